@@ -296,6 +296,43 @@ MOE_API moe_status moe_shared_expert_ex(const void* x, const moe_experts_w* Ws, 
                                         const moe_exec_cfg* exec, float* y_shared, void* ws,
                                         size_t ws_bytes, moe_stream_t stream);
 
+/* A whole MoE layer for a few tokens in one kernel launch.
+ *   y = bf16_rn(out_scale * sum_j w_j down_e(act(up_e(x))) + shared(x) + residual)
+ * with the routing of moe_route_ex: at decode sizes the layer is one pass over
+ * the picked experts' weights, and this call makes it without moe_forward's
+ * separate router, plan, gather, up, down and finalize kernels.
+ *   moe_layer   what stays the same from step to step: router, experts, shared
+ *               expert (Ws, Is; Is = 0: none, Ws unused; layout as for
+ *               moe_shared_expert, with W's fmt and act), scalars.
+ *   x           bf16 (T, H).  Routing reads x, or logits (fp32 (T, E)) when given.
+ *   residual    bf16 (T, H) or NULL, added to the finished sum in fp32.
+ *   topk_idx, topk_w, y   outputs as of moe_forward_ex.  y may be residual or x.
+ * Sizes: moe_dims' limits, T <= MOE_DECODE_MAX_T and T * H <= 65536
+ * (MOE_ERR_SHAPE otherwise: moe_forward takes those).
+ * Arithmetic: logits, scores and weights in 64-bit (topk_w rounded once to fp32),
+ * so picks differ from moe_route's fp32 picks only where two scores are within
+ * its rounding; activations are rounded once to bf16; sums are fp32 and in a
+ * fixed order for a given set of picks (no atomics), y is rounded once.
+ * Workspace: moe_decode_workspace_bytes(d, Is); its first 256 bytes must be
+ * zero before the first call, and every call leaves them zero.  Calls that
+ * share a workspace must not overlap on the GPU.  The launch is cooperative
+ * (one CTA per SM, all resident); waits between CTAs are bounded and report
+ * device error 2. */
+#define MOE_DECODE_MAX_T 16
+typedef struct {
+    const float* w_router;
+    const float* expert_bias; /* may be NULL */
+    moe_experts_w W;
+    moe_experts_w Ws;
+    int32_t Is;
+    float eps, router_scale, out_scale;
+    moe_router_cfg router;
+} moe_layer;
+MOE_API size_t moe_decode_workspace_bytes(const moe_dims* d, int32_t Is);
+MOE_API moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void* x, const float* logits,
+                              const void* residual, int32_t* topk_idx, float* topk_w, void* y, void* ws,
+                              size_t ws_bytes, moe_stream_t stream);
+
 /* moe_forward with HOST buffers for the token rows: x_host (T, H) bf16 is
  * copied to x_dev, the block runs, and y_dev is copied back to y_host (T, H)
  * bf16, all on `stream`; the call then synchronises `stream`.  x_host/y_host

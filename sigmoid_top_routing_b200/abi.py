@@ -24,6 +24,7 @@ MOE_COMBINE_ATOMIC, MOE_COMBINE_ORDERED = 0, 1
 MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
 MOE_STAGE_ROUTE, MOE_STAGE_PLAN, MOE_STAGE_UP, MOE_STAGE_DOWN, MOE_STAGE_FINAL, MOE_STAGE_GATHER = range(6)
 MOE_TILE_M = 128
+MOE_DECODE_MAX_T = 16
 
 
 class moe_dims(ctypes.Structure):
@@ -55,6 +56,12 @@ class moe_ws_layout(ctypes.Structure):
                 ("total", c_size_t)]
 
 
+class moe_layer(ctypes.Structure):
+    _fields_ = [("w_router", c_void_p), ("expert_bias", c_void_p), ("W", moe_experts_w), ("Ws", moe_experts_w),
+                ("Is", c_int32), ("eps", c_float), ("router_scale", c_float), ("out_scale", c_float),
+                ("router", moe_router_cfg)]
+
+
 # name -> (restype, argtypes), exactly the declarations of include/moe.h
 PROTOTYPES = {
     "moe_workspace_bytes": (c_size_t, [POINTER(moe_dims), c_int32]),
@@ -83,6 +90,9 @@ PROTOTYPES = {
                                     c_size_t, c_void_p]),
     "moe_shared_expert_ex": (c_int32, [c_void_p, POINTER(moe_experts_w), POINTER(moe_dims),
                                        POINTER(moe_exec_cfg), c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_decode_workspace_bytes": (c_size_t, [POINTER(moe_dims), c_int32]),
+    "moe_decode": (c_int32, [POINTER(moe_layer), POINTER(moe_dims), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                             c_void_p, c_void_p, c_size_t, c_void_p]),
     "moe_forward_host": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, POINTER(moe_dims), c_float,
                                    c_float, c_float, POINTER(moe_experts_w), c_void_p, c_void_p,
                                    POINTER(moe_plan_t), c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),

@@ -20,7 +20,7 @@ __all__ = [
     "moe_experts", "moe_forward", "moe_forward_host", "moe_shared_expert", "moe_set_dispatch", "moe_set_combine",
     "moe_device_error",
     "moe_last_error", "moe_version", "new_plan", "new_workspace", "dims", "moe_profile_hook",
-    "moe_last_launch_count", "exec_cfg", "moe_experts_ex",
+    "moe_last_launch_count", "exec_cfg", "moe_experts_ex", "DecodeLayer", "moe_decode_workspace_bytes",
 ]
 
 
@@ -232,6 +232,101 @@ def moe_forward_host(x_host: torch.Tensor, x_dev, W: ExpertWeights, w_router, ex
                                   _ptr(topk_idx), _ptr(topk_w), ctypes.byref(cp), _ptr(y_dev),
                                   y_host.data_ptr(), _ptr(ws), ws.numel(), _stream(stream)), "moe_forward_host")
     return y_host
+
+
+def moe_decode_workspace_bytes(d: abi.moe_dims, Is: int = 0) -> int:
+    return int(load().moe_decode_workspace_bytes(ctypes.byref(d), Is))
+
+
+def _want(name: str, t: Optional[torch.Tensor], shape, dtypes, device) -> None:
+    """Refuse a tensor that the library would read with another shape or type."""
+    if t is None:
+        return
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {tuple(shape)} of {dtypes[0]}, got {tuple(t.shape)} of {t.dtype}")
+
+
+def _check_weights(name: str, W: ExpertWeights, E: int, I: int, H: int, device) -> None:
+    n1 = 2 * I if W.act == abi.MOE_ACT_SWIGLU else I
+    for i, n, K in ((1, n1, H), (2, H, I)):
+        w, sc = getattr(W, f"w{i}"), getattr(W, f"w{i}_scale")
+        if W.fmt == abi.MOE_W_BF16:
+            _want(f"{name}.w{i}", w, (E, n, K), (torch.bfloat16,), device)
+        elif W.fmt == abi.MOE_W_AFFINE4_G64:
+            _want(f"{name}.w{i}", w, (E, n, K // 8), (torch.int32, torch.uint32), device)
+            _want(f"{name}.w{i}_scale", sc, (E, n, K // 64), (torch.bfloat16,), device)
+            _want(f"{name}.w{i}_bias", getattr(W, f"w{i}_bias"), (E, n, K // 64), (torch.bfloat16,), device)
+        else:
+            _want(f"{name}.w{i}", w, (E, n, K // 2), (torch.uint8,), device)
+            _want(f"{name}.w{i}_scale", sc, (E, n, K // 16), (torch.uint8,), device)
+            _want(f"{name}.w{i}_global", getattr(W, f"w{i}_global"), (E,), (torch.float32,), device)
+
+
+class DecodeLayer:
+    """A whole MoE layer for a few tokens, one kernel launch a call (``moe_decode``).
+
+    Holds what stays the same from step to step: the router, the experts, an
+    optional shared expert (``Ws`` of width ``Is``, same format and activation),
+    the scalars, and a workspace for up to ``max_tokens`` tokens.  ``layer(x)``
+    returns ``(y, topk_idx, topk_w)``.  The workspace is the layer's own: its
+    calls must not overlap on the GPU (calls on several streams, or graphs that
+    replay at once, each need a layer of their own).  The tensors given here are
+    kept, not copied: new values in them count from the next call on.
+    """
+
+    def __init__(self, W: ExpertWeights, w_router=None, expert_bias=None, *, E: int, k: int, I: int,
+                 Ws: Optional[ExpertWeights] = None, Is: int = 0, eps: float = 1e-6, router_scale: float = 1.0,
+                 out_scale: float = 1.0, score: str = "sigmoid", norm_topk: bool = True,
+                 max_tokens: int = abi.MOE_DECODE_MAX_T):
+        if W.w2.dim() != 3:
+            raise ValueError("w2: expected (E, H, ...)")
+        self.device = dev = W.w2.device
+        self.H, self.E, self.k, self.I = W.w2.shape[1], E, k, I
+        if (Ws is None) != (Is == 0):
+            raise ValueError("give Ws and Is together")
+        _want("w_router", w_router, (E, self.H), (torch.float32,), dev)
+        _want("expert_bias", expert_bias, (E,), (torch.float32,), dev)
+        _check_weights("W", W, E, I, self.H, dev)
+        if Ws is not None:
+            _check_weights("Ws", Ws, 1, Is, self.H, dev)
+        self._keep = (W, Ws, w_router, expert_bias)
+        self.max_tokens = max_tokens
+        with torch.cuda.device(dev):
+            n = moe_decode_workspace_bytes(abi.moe_dims(max_tokens, self.H, E, k, I), Is)
+        if n == 0:
+            raise ValueError(f"sizes of the layer: {moe_last_error()}")
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=dev)   # the first 256 bytes start at zero
+        self._layer = abi.moe_layer(_ptr(w_router), _ptr(expert_bias), W.c_struct(),
+                                    Ws.c_struct() if Ws is not None else abi.moe_experts_w(), Is, eps, router_scale,
+                                    out_scale, router_cfg(score, norm_topk))
+
+    def __call__(self, x, *, residual=None, logits=None, y=None, topk_idx=None, topk_w=None, stream=None):
+        dev, k = self.device, self.k
+        T = x.shape[0]
+        if T > self.max_tokens:
+            raise ValueError(f"{T} tokens, but the layer was made for max_tokens = {self.max_tokens}")
+        _want("x", x, (T, self.H), (torch.bfloat16,), dev)
+        _want("residual", residual, (T, self.H), (torch.bfloat16,), dev)
+        _want("logits", logits, (T, self.E), (torch.float32,), dev)
+        _want("y", y, (T, self.H), (torch.bfloat16,), dev)
+        _want("topk_idx", topk_idx, (T, k), (torch.int32,), dev)
+        _want("topk_w", topk_w, (T, k), (torch.float32,), dev)
+        y = torch.empty_like(x) if y is None else y
+        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_idx is None else topk_idx
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
+        d = abi.moe_dims(T, self.H, self.E, k, self.I)
+        if torch.cuda.current_device() != dev.index:
+            with torch.cuda.device(dev):
+                return self._run(d, x, logits, residual, topk_idx, topk_w, y, stream)
+        return self._run(d, x, logits, residual, topk_idx, topk_w, y, stream)
+
+    def _run(self, d, x, logits, residual, topk_idx, topk_w, y, stream):
+        check(load().moe_decode(ctypes.byref(self._layer), ctypes.byref(d), x.data_ptr(), _ptr(logits), _ptr(residual),
+                                topk_idx.data_ptr(), topk_w.data_ptr(), y.data_ptr(), self.ws.data_ptr(),
+                                self.ws.numel(), _stream(stream)), "moe_decode")
+        return y, topk_idx, topk_w
 
 
 def moe_profile_hook(ev_begin, ev_end, stage: int) -> None:

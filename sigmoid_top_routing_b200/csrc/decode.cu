@@ -1,0 +1,955 @@
+// A whole routed MoE layer for a few tokens (T <= 16) in one kernel launch:
+// router, selection, expert up projections, activation, expert down
+// projections, weighted sum, shared expert and residual.
+//
+//   L = x . Wr^T;  s = sigmoid(L) or softmax(L);  picks = top-k of s + b;
+//   w = s / (sum s + eps) * scale;  h_j = bf16(act(W1[e_j] x));
+//   y = bf16(out_scale * sum_j w_j W2[e_j] h_j + W2s act(W1s x) + residual)
+//
+// At this size the layer is one pass over the picked experts' weights, so the
+// kernel is built around that stream.  One CTA per SM; a producer warp copies
+// weight rows into a ring of stages with bulk copies and 16 consumer warps, in
+// 4 groups of 4, multiply them with the token rows on m16n8k16 MMAs (the token
+// count is at most the MMA's N, so the tensor cores idle either way; see
+// stream.cuh for the stage layout).
+//
+//   up    The active experts' features (I per routed expert) form one list;
+//         every CTA takes an equal contiguous part of it, in tiles of 8
+//         features (SwiGLU: 8 gate and 8 up rows, which meet in one thread) or
+//         16 (relu^2).  h goes to global memory, one row per routed pair.
+//   down  Every CTA owns H / CTAs rows of y and runs them through all active
+//         experts, so y needs no atomics and no second pass: partial sums
+//         stay in shared memory and one fixed-order sum ends the row.
+//
+// Two grid barriers (after the logits, after h) join the phases; the launch is
+// cooperative, so all CTAs are resident and the waits end.  Neither stops the
+// stream of weights for long: the producer fetches the shared expert's rows
+// before the routing is known and the down rows before h is.
+//
+// Router sums and scores are 64-bit: E * H * T is small here, and picks are
+// then those of the real-number scores up to ties.
+//
+// Bound: HBM for bf16 experts from a few tokens on; latency (barriers, first
+// loads, launch) at one token.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "launch.h"
+#include "stream.cuh"
+
+namespace moe {
+namespace {
+
+using namespace stream;
+
+constexpr int kGroups = 4;                      // consumer groups, each on a tile of its own
+constexpr int kGw = 4;                          // warps of a group: they share a tile's k
+constexpr int kCw = kGroups * kGw;              // consumer warps
+constexpr int kCThreads = kCw * 32;
+constexpr int kThreads = kCThreads + 32;        // + the producer warp
+constexpr int kMaxE = 257;                      // 256 experts and the shared one
+constexpr int kMaxK = 32;
+constexpr int kMaxStages = 16;
+
+struct WMat {                                   // one weight tensor of the experts
+    const unsigned char* w;
+    const unsigned char* scale;
+    const unsigned char* bias;
+    const float* glob;
+    int rows, K;                                // rows per expert, row length
+};
+
+struct DecodeArgs {
+    const uint16_t* x;
+    const float* logits;
+    const float* w_router;
+    const float* ebias;
+    const uint16_t* residual;
+    WMat W1, W2, S1, S2;
+    int T, H, E, k, I, Is;
+    float eps, scale, out_scale, limit, limit_s;
+    int softmax, no_norm;
+    int32_t* idx;
+    float* w;
+    uint16_t* y;
+    uint32_t* sync;                             // [0] barrier arrivals, [1] exits; zero between calls
+    double* lg;                                 // (T, E)
+    uint16_t* h;                                // (T k, I)
+    uint16_t* hs;                               // (T, Is)
+    int stages;                                 // ring slots per group
+    StageDims sd;
+    uint32_t wait_limit;
+    int* err;
+};
+
+template <int NT>
+struct Layout {                                 // shared memory (byte offsets)
+    static constexpr int kTok = 8 * NT;
+    static constexpr int kMask = 0;                                   // kMaxE words: tokens of an expert
+    static constexpr int kList = kMask + 1040;                        // active expert ids
+    static constexpr int kPick = kList + 1040;                        // [kTok][kMaxK] expert of a pick
+    static constexpr int kWt = kPick + kTok * kMaxK * 4;              // [kTok][kMaxK] routing weight
+    static constexpr int kSlot = kWt + kTok * kMaxK * 4;              // [kTok][256] bytes: pick number of an expert
+    static constexpr int kMisc = kSlot + kTok * 256;                  // active count, abort flag
+    static constexpr int kBar = kMisc + 16;
+    static constexpr int kRed = kBar + 2 * kMaxStages * 8;            // group sums; later y sums per warp
+    static constexpr int kRedBuf = kGw * kRows * kTok * 4;            // one buffer of one group
+    static constexpr int kRedBytes = kGroups * 2 * kRedBuf;
+    static constexpr int kYs = kRed + kRedBytes;                      // shared expert's y sums, one per warp of a group
+    static constexpr int kX = (kYs + kGw * kRows * kTok * 4 + 127) & ~127;
+    static_assert(kCw * kRows * kTok * 4 <= kRedBytes, "y sums fit the group-sum buffers");
+};
+
+MOE_DEV uint64_t key64(double c) {              // order of c; NaN lowest (1), -0 == +0
+    if (c != c) return 1ull;
+    if (c == 0.0) c = 0.0;
+    const uint64_t u = (uint64_t)__double_as_longlong(c);
+    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+
+// Picks of one token by one warp; lane holds experts lane + 32 i.
+MOE_DEV void select_token(const DecodeArgs& a, int t, int* pick, float* wt, unsigned char* slot, uint32_t* mask,
+                          bool write) {
+    const int lane = threadIdx.x & 31;
+    double s[8];
+    uint64_t key[8];
+    const int ne = (a.E + 31) / 32;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int e = lane + 32 * i;
+        s[i] = 0.0;
+        if (i < ne && e < a.E)
+            s[i] = a.logits ? (double)__ldg(a.logits + (size_t)t * a.E + e) : __ldcg(a.lg + (size_t)t * a.E + e);
+    }
+    if (a.softmax) {                            // a NaN logit makes the row's scores NaN (through the sum)
+        double m = -INFINITY, z = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (lane + 32 * i < a.E) m = fmax(m, s[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (lane + 32 * i < a.E) {
+                s[i] = exp(s[i] - m);
+                z += s[i];
+            }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = z == z ? s[i] / z : z;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < ne) s[i] = 1.0 / (1.0 + exp(-s[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int e = lane + 32 * i;
+        key[i] = e < a.E ? key64(s[i] + (a.ebias ? (double)__ldg(a.ebias + e) : 0.0)) : 0ull;
+    }
+    int my_e = 0;
+    double my_s = 0.0, sum = 0.0;
+    for (int j = 0; j < a.k; ++j) {
+        uint64_t best = key[0];
+        int bi = 0;
+        double bs = s[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            if (key[i] > best) { best = key[i]; bi = i; bs = s[i]; }
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
+        const bool ch = (uint32_t)(best >> 32) == hi;
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, ch ? (uint32_t)best : 0u);
+        const bool win = ch && (uint32_t)best == lo;
+        const uint32_t e = __reduce_min_sync(0xffffffffu, win ? (uint32_t)(lane + 32 * bi) : 0xffffu);
+        const double sj = __shfl_sync(0xffffffffu, bs, e & 31);
+        if (lane == (int)(e & 31)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i == (int)(e >> 5)) key[i] = 0ull;    // picked: below every NaN
+        }
+        if (lane == j) { my_e = (int)e; my_s = sj; }
+        sum += sj;                              // rank order
+    }
+    if (lane < a.k) {
+        const double w = a.no_norm ? my_s * a.scale : my_s / (sum + (double)a.eps) * a.scale;
+        pick[lane] = my_e;
+        wt[lane] = (float)w;
+        slot[my_e] = (unsigned char)lane;
+        atomicOr(mask + my_e, 1u << t);
+        if (write) {
+            a.idx[(size_t)t * a.k + lane] = my_e;
+            a.w[(size_t)t * a.k + lane] = (float)w;
+        }
+    }
+}
+
+// The c-th set bit of m (c < popc(m)).
+MOE_DEV int nth_bit(uint32_t m, int c) {
+    for (int i = 0; i < c; ++i) m &= m - 1;
+    return __ffs(m) - 1;
+}
+
+// A unit of work: rows of one expert against all its tokens.
+struct Unit {
+    int e;                                      // expert; a.E: the shared one
+    int n;                                      // rows (per half when dual)
+    int f0;                                     // first feature (up) or row of y (down)
+    size_t row0, row1;                          // first weight row; of the up half when dual
+};
+
+MOE_DEV int chunks_of(int K, const StageDims& sd) { return (K + sd.chunk - 1) / sd.chunk; }
+
+// Copies k [k0, k0 + kc) of a unit's rows (and their scales) into a stage.
+template <int FMT>
+MOE_DEV void issue_stage(const StageDims& sd, const WMat& m, const Unit& u, bool dual, int c, uint32_t dst, uint64_t* bar, uint64_t pol) {
+    using F = Fmt<FMT>;
+    const int lane = threadIdx.x & 31;
+    const int k0 = c * sd.chunk, kc = min(sd.chunk, m.K - k0);
+    bool code = false;
+    size_t R = 0;
+    if (lane < kRows) {
+        const int half = dual ? lane >> 3 : 0, loc = dual ? lane & 7 : lane;
+        code = loc < u.n;
+        R = (half ? u.row1 : u.row0) + loc;
+    }
+    const uint32_t rb = (uint32_t)F::row_bytes(kc);
+    uint32_t bytes = code ? rb : 0, sb = 0, sdst = 0;
+    size_t s0 = 0;
+    if (FMT != kBf16) {
+        // scale rows start anywhere: copy the 16-byte aligned span around them
+        // (the arrays hold a multiple of 128 bytes, so it stays inside)
+        const size_t SB = F::scale_bytes(m.K);
+        size_t b = 0, e = 0;
+        if (m.K <= sd.chunk) {                  // whole rows: the unit's rows are one span per half
+            if (lane == 16 || (lane == 17 && dual)) {
+                b = (lane == 17 ? u.row1 : u.row0) * SB;
+                e = b + u.n * SB;
+                sdst = sd.codes + (lane - 16) * (sd.area / 2);
+            }
+        } else if (code) {
+            b = R * SB + F::scale_bytes(k0);
+            e = b + F::scale_bytes(kc);
+            sdst = sd.codes + lane * sd.slot;
+        }
+        if (e > b) {
+            s0 = b & ~size_t(15);
+            sb = (uint32_t)(((e + 15) & ~size_t(15)) - s0);
+        }
+        bytes += sb * (FMT == kAffine ? 2 : 1);
+    }
+    const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+    if (lane == 0) mbar_arrive_expect_tx(bar, total);
+    __syncwarp();
+    if (code) bulk_load(dst + lane * sd.row_stride, m.w + R * F::row_bytes(m.K) + F::row_bytes(k0), rb, bar, pol);
+    if (FMT != kBf16 && sb) {
+        bulk_load(dst + sdst, m.scale + s0, sb, bar, pol);
+        if (FMT == kAffine) bulk_load(dst + sdst + sd.area, m.bias + s0, sb, bar, pol);
+    }
+}
+
+// Stage address of the scales of weight row R (MMA row r) of this unit.
+template <int FMT>
+MOE_DEV uint32_t scale_addr(const StageDims& sd, const WMat& m, const Unit& u, bool dual, int r, int c, uint32_t st) {
+    using F = Fmt<FMT>;
+    const int half = dual ? r >> 3 : 0, loc = dual ? r & 7 : r;
+    const size_t base = half ? u.row1 : u.row0;
+    const size_t SB = F::scale_bytes(m.K);
+    if (m.K <= sd.chunk) return st + sd.codes + half * (sd.area / 2) + uint32_t((base * SB) & 15) + loc * (uint32_t)SB;
+    return st + sd.codes + r * sd.slot + uint32_t(((base + loc) * SB + F::scale_bytes(c * sd.chunk)) & 15);
+}
+
+// One step of the products: rows g and g + 8 of the stage against the 8 NT
+// columns held in b (per column 16 bytes bf16, 32 bytes 4-bit).
+template <int FMT, int NT>
+MOE_DEV void step(const StageDims& sd, uint32_t st, int s, uint32_t sc0, uint32_t sc1, const uint4 (&b)[NT][FMT == kBf16 ? 1 : 2],
+                  int ntn, float (&acc)[NT][4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t r0 = st + g * sd.row_stride, r1 = r0 + 8 * sd.row_stride;
+    if constexpr (FMT == kBf16) {
+        const uint4 p = lds128(r0 + s * 64 + t * 16), q = lds128(r1 + s * 64 + t * 16);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            if (n < ntn) {
+                mma_bf16(acc[n], p.x, q.x, p.y, q.y, b[n][0].x, b[n][0].y);
+                mma_bf16(acc[n], p.z, q.z, p.w, q.w, b[n][0].z, b[n][0].w);
+            }
+    } else if constexpr (FMT == kAffine) {
+        // sum_k w x = s sum_k (128 + q) x + (b - 128 s) sum_k x over the step,
+        // which is one group of 64; sum_k x by MMAs against ones
+        const uint2 p = lds64(r0 + s * 32 + t * 8), q = lds64(r1 + s * 32 + t * 8);
+        const float s0 = bf16f(lds_u16(sc0 + s * 2)), s1 = bf16f(lds_u16(sc1 + s * 2));
+        const float b0 = bf16f(lds_u16(sc0 + sd.area + s * 2)) - 128.0f * s0;
+        const float b1 = bf16f(lds_u16(sc1 + sd.area + s * 2)) - 128.0f * s1;
+        constexpr uint32_t one = 0x3F803F80u;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            if (n < ntn) {
+                float c[4] = {}, x[4] = {};
+                const uint4 u = b[n][0], v = b[n][1];
+                mma_bf16(c, nib_pair(p.x, 0), nib_pair(q.x, 0), nib_pair(p.x, 1), nib_pair(q.x, 1), u.x, u.y);
+                mma_bf16(x, one, one, one, one, u.x, u.y);
+                mma_bf16(c, nib_pair(p.x, 2), nib_pair(q.x, 2), nib_pair(p.x, 3), nib_pair(q.x, 3), u.z, u.w);
+                mma_bf16(x, one, one, one, one, u.z, u.w);
+                mma_bf16(c, nib_pair(p.y, 0), nib_pair(q.y, 0), nib_pair(p.y, 1), nib_pair(q.y, 1), v.x, v.y);
+                mma_bf16(x, one, one, one, one, v.x, v.y);
+                mma_bf16(c, nib_pair(p.y, 2), nib_pair(q.y, 2), nib_pair(p.y, 3), nib_pair(q.y, 3), v.z, v.w);
+                mma_bf16(x, one, one, one, one, v.z, v.w);
+                acc[n][0] += s0 * c[0] + b0 * x[0];
+                acc[n][1] += s0 * c[1] + b0 * x[1];
+                acc[n][2] += s1 * c[2] + b1 * x[0];
+                acc[n][3] += s1 * c[3] + b1 * x[1];
+            }
+    } else {
+        // a lane's 16 k are one scale block: e2m1 * e4m3 exactly in bf16
+        const uint2 p = lds64(r0 + s * 32 + t * 8), q = lds64(r1 + s * 32 + t * 8);
+        const uint32_t e0 = lds_u8(sc0 + s * 4 + t), e1 = lds_u8(sc1 + s * 4 + t);
+        const uint32_t s0 = e4m3x2_to_f16x2(e0 | (e0 << 8)), s1 = e4m3x2_to_f16x2(e1 | (e1 << 8));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t u[4], v[4];
+            e2m1x8_to_f16(half ? p.y : p.x, u);
+            e2m1x8_to_f16(half ? q.y : q.x, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u[i] = f16x2_to_bf16x2(hmul2_u32(u[i], s0));
+                v[i] = f16x2_to_bf16x2(hmul2_u32(v[i], s1));
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                if (n < ntn) {
+                    const uint4 x = b[n][half];
+                    mma_bf16(acc[n], u[0], v[0], u[1], v[1], x.x, x.y);
+                    mma_bf16(acc[n], u[2], v[2], u[3], v[3], x.z, x.w);
+                }
+        }
+    }
+}
+
+template <int FMT, int NT, bool DUAL>
+__global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ DecodeArgs a) {
+    using F = Fmt<FMT>;
+    using L = Layout<NT>;
+    constexpr int TT = L::kTok;
+    constexpr int kFeat = DUAL ? 8 : kRows;     // features of an up tile
+    constexpr int kB = FMT == kBf16 ? 1 : 2;    // 16-byte pieces of a column per step
+    // steps whose token operand a down warp requests before it waits for the weights
+    constexpr int kAhead = FMT == kBf16 ? 4 : (NT == 1 ? 4 : 2);
+    extern __shared__ __align__(128) unsigned char sm[];
+    uint32_t* s_mask = reinterpret_cast<uint32_t*>(sm + L::kMask);
+    int* s_list = reinterpret_cast<int*>(sm + L::kList);
+    int* s_pick = reinterpret_cast<int*>(sm + L::kPick);
+    float* s_wt = reinterpret_cast<float*>(sm + L::kWt);
+    unsigned char* s_slot = sm + L::kSlot;
+    int* s_nact = reinterpret_cast<int*>(sm + L::kMisc);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar);
+    uint64_t* empty = full + kMaxStages;
+    float* s_red = reinterpret_cast<float*>(sm + L::kRed);
+    float* s_ys = reinterpret_cast<float*>(sm + L::kYs);
+    const int xstride = a.H * 2 + F::kXPad;
+    const uint32_t xs = smem_u32(sm + L::kX);
+    const uint32_t ring = xs + ((a.T * xstride + 127) & ~127);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = gridDim.x, cta = blockIdx.x;
+    const int Sg = a.stages;                    // ring slots of one group (its own: it alone fills and frees them in order)
+    for (int i = tid; i < kMaxE; i += kThreads) s_mask[i] = 0;
+    if (tid == 0) {
+        for (int i = 0; i < kGroups * Sg; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kGw);
+        }
+        *s_abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+
+    // This CTA's parts: features of the shared expert, features of the routed
+    // experts' list (once it is known), rows of y.
+    const int sf0 = (int)((long long)cta * a.Is / G), sf1 = (int)((long long)(cta + 1) * a.Is / G);
+    const int yr0 = (int)((long long)cta * a.H / G), yr1 = (int)((long long)(cta + 1) * a.H / G);
+    const int ytiles = (yr1 - yr0 + kRows - 1) / kRows;
+    const int up_chunks = chunks_of(a.H, a.sd);
+    const int s_units = (sf1 - sf0 + kFeat - 1) / kFeat;
+
+    auto shared_up = [&](int i) {               // i-th tile of the shared expert's features
+        Unit u;
+        u.e = a.E;
+        u.f0 = sf0 + i * kFeat;
+        u.n = min(kFeat, sf1 - u.f0);
+        u.row0 = u.f0;
+        u.row1 = (size_t)a.Is + u.f0;
+        return u;
+    };
+    auto routed_up = [&](long long f, long long f1, Unit& u) {   // tile at list position f; returns the next f
+        const int li = (int)(f / a.I), off = (int)(f - (long long)li * a.I);
+        u.e = s_list[li];
+        u.f0 = off;
+        u.n = (int)min((long long)min(kFeat, a.I - off), f1 - f);
+        u.row0 = (size_t)u.e * a.W1.rows + off;
+        u.row1 = u.row0 + a.I;
+        return f + u.n;
+    };
+    auto down_unit = [&](int tile, int li, int nact) {           // li == nact: the shared expert
+        Unit u;
+        const int b = (int)((long long)tile * (yr1 - yr0) / ytiles), e = (int)((long long)(tile + 1) * (yr1 - yr0) / ytiles);
+        u.e = li < nact ? s_list[li] : a.E;
+        u.f0 = yr0 + b;
+        u.n = e - b;
+        u.row0 = (li < nact ? (size_t)u.e * a.H : 0) + u.f0;
+        u.row1 = u.row0;
+        return u;
+    };
+
+    if (warp == kCw) {
+        // -------------------------------------------------------- producer
+        const uint64_t pol = policy_evict_first();
+        int cnt[kGroups] = {};                  // stages issued, per group
+        bool ok = true;
+        auto push = [&](int gr, const WMat& m, const Unit& u, bool dual, int c) {
+            const int q = cnt[gr], s = gr * Sg + q % Sg;
+            if (q >= Sg) {
+                const bool got = mbar_wait(&empty[s], (uint32_t)((q / Sg - 1) & 1), s_abort, a.wait_limit);
+                if (!__all_sync(0xffffffffu, got)) ok = false;
+            }
+            if (!ok) return;
+            issue_stage<FMT>(a.sd, m, u, dual, c, ring + s * a.sd.bytes, &full[s], pol);
+            ++cnt[gr];
+        };
+        // Units go to the groups in turn; the stages of kGroups units are
+        // issued chunk by chunk, so all groups' slots fill at one rate.
+        // shared(first, only_free): the shared expert's stages from number
+        // `first` on; with only_free it stops where it would wait.
+        auto shared = [&](int first, bool only_free) {
+            int q = 0;
+            for (int b = 0; b < s_units; b += kGroups)
+                for (int c = 0; c < up_chunks; ++c)
+#pragma unroll
+                    for (int gr = 0; gr < kGroups; ++gr)
+                        if (b + gr < s_units && q++ >= first && ok) {
+                            if (only_free && cnt[gr] >= Sg) return q - 1;
+                            push(gr, a.S1, shared_up(b + gr), DUAL, c);
+                        }
+            return q;
+        };
+        const int pre = shared(0, true);        // needs no routing
+        __syncthreads();                        // routing tables ready
+        shared(pre, false);
+        const int nact = *s_nact;
+        const long long Fr = (long long)nact * a.I;
+        const long long f1 = (cta + 1) * Fr / G;
+        for (long long f = cta * Fr / G; f < f1 && ok;) {
+            Unit u[kGroups];
+            int nu = 0;
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr)
+                if (f < f1) {
+                    f = routed_up(f, f1, u[gr]);
+                    nu = gr + 1;
+                }
+            for (int c = 0; c < up_chunks && ok; ++c)
+#pragma unroll
+                for (int gr = 0; gr < kGroups; ++gr)
+                    if (gr < nu && ok) push(gr, a.W1, u[gr], DUAL, c);
+        }
+        const int nd = nact + (a.Is > 0), i_chunks = chunks_of(a.I, a.sd), is_chunks = chunks_of(a.Is, a.sd);
+        for (int b = 0; b < ytiles * nd && ok; b += kGroups) {
+            Unit u[kGroups];
+            int nch[kGroups], most = 0;
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr) {
+                const int i = b + gr;
+                nch[gr] = 0;
+                if (i < ytiles * nd) {
+                    u[gr] = down_unit(i / nd, i % nd, nact);
+                    nch[gr] = i % nd < nact ? i_chunks : is_chunks;
+                    most = max(most, nch[gr]);
+                }
+            }
+            for (int c = 0; c < most && ok; ++c)
+#pragma unroll
+                for (int gr = 0; gr < kGroups; ++gr)
+                    if (c < nch[gr] && ok) push(gr, u[gr].e < a.E ? a.W2 : a.S2, u[gr], false, c);
+        }
+        if (!ok) {
+            if (lane == 0) report_error(a.err, kErrWaitExpired);
+            *s_abort = 1;
+        }
+        // every copy issued lands before the CTA can exit
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr)
+            for (int q = max(0, cnt[gr] - Sg); q < cnt[gr]; ++q)
+                mbar_wait(&full[gr * Sg + q % Sg], (uint32_t)((q / Sg) & 1), nullptr, a.wait_limit);
+    } else {
+        // -------------------------------------------------------- consumers
+        const int grp = warp / kGw, gw = warp % kGw, gt = tid % (kGw * 32);
+        const int g = lane >> 2, t4 = lane & 3;
+        bool dead = false;
+        uint32_t target = 0;
+        auto arrive = [&]() {                   // one thread, after a barrier of all consumers
+            __threadfence();
+            atomicAdd(a.sync, 1u);
+        };
+        auto grid_wait = [&]() {                // one thread
+            bool ok = false;
+            for (uint32_t i = 0; i < a.wait_limit && !ok; ++i) {
+                uint32_t v;
+                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.sync) : "memory");
+                ok = v >= target;
+            }
+            if (!ok) {
+                report_error(a.err, kErrWaitExpired);
+                *s_abort = 1;
+            }
+            __threadfence();
+        };
+        // ---- router: CTA e computes expert e's logits for all tokens
+        if (!a.logits) {
+            double* s_d = reinterpret_cast<double*>(s_red);      // [kCw][TT]
+            for (int e = cta; e < a.E; e += G) {
+                double acc[TT];
+#pragma unroll
+                for (int t = 0; t < TT; ++t) acc[t] = 0.0;
+                for (int k = tid * 4; k < a.H; k += kCThreads * 4) {
+                    const float4 w = __ldg(reinterpret_cast<const float4*>(a.w_router + (size_t)e * a.H + k));
+#pragma unroll
+                    for (int t = 0; t < TT; ++t)
+                        if (t < a.T) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(a.x + (size_t)t * a.H + k);
+                            acc[t] = fma((double)w.x, (double)bf16lo(v.x), acc[t]);
+                            acc[t] = fma((double)w.y, (double)bf16hi(v.x), acc[t]);
+                            acc[t] = fma((double)w.z, (double)bf16lo(v.y), acc[t]);
+                            acc[t] = fma((double)w.w, (double)bf16hi(v.y), acc[t]);
+                        }
+                }
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+                    if (t < a.T) {
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+                        if (lane == 0) s_d[warp * TT + t] = acc[t];
+                    }
+                named_bar(5, kCThreads);
+                if (tid < a.T) {
+                    double v = 0.0;
+                    for (int w = 0; w < kCw; ++w) v += s_d[w * TT + tid];
+                    __stcg(a.lg + (size_t)tid * a.E + e, v);
+                }
+                named_bar(5, kCThreads);
+            }
+            target += G;
+            if (tid == 0) arrive();
+        }
+        // ---- token rows into shared memory (while the other CTAs' logits arrive)
+        for (int i = tid; i < a.T * (a.H / 8); i += kCThreads) {
+            const int t = i / (a.H / 8), c = i - t * (a.H / 8);
+            uint4 v = *(reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H) + c);
+            if (FMT == kAffine)                 // pairs (j, j + 4)
+                v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                               __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+            *reinterpret_cast<uint4*>(sm + L::kX + (size_t)t * xstride + c * 16) = v;
+        }
+        if (!a.logits && tid == 0) grid_wait();
+        named_bar(5, kCThreads);
+        // ---- selection: every CTA picks for all tokens, a warp per token
+        if (warp < a.T)
+            select_token(a, warp, s_pick + warp * kMaxK, s_wt + warp * kMaxK, s_slot + warp * 256, s_mask, cta == 0);
+        named_bar(5, kCThreads);
+        if (warp == 0) {
+            int n = 0;
+            for (int e0 = 0; e0 < a.E; e0 += 32) {
+                const int e = e0 + lane;
+                const bool on = e < a.E && s_mask[e] != 0;
+                const uint32_t bal = __ballot_sync(0xffffffffu, on);
+                if (on) s_list[n + __popc(bal & ((1u << lane) - 1))] = e;
+                n += __popc(bal);
+            }
+            if (lane == 0) {
+                *s_nact = n;
+                s_mask[a.E] = (1u << a.T) - 1;
+            }
+        }
+        __syncthreads();                        // routing tables ready (producer too)
+        const int nact = *s_nact;
+        int cnt = 0;                            // stages this group has passed
+        // Columns: token of this lane's operand column per 8-token block, and
+        // the row of its activations.
+        auto col_token = [&](uint32_t mask, int ncol, int c) { return nth_bit(mask, c < ncol ? c : 0); };
+        float* red = s_red + grp * 2 * (L::kRedBuf / 4);
+        int rbuf = 0;
+
+        // the products of one unit: acc = rows x columns over this warp's share of k
+        auto run_unit = [&](const WMat& m, const Unit& u, bool dual, bool from_x, const uint16_t* (&hp)[NT],
+                            const uint32_t (&xp)[NT], int ntn, float (&acc)[NT][4]) {
+            const int nch = chunks_of(m.K, a.sd);
+            for (int c = 0; c < nch; ++c, ++cnt) {
+                const int s = grp * Sg + cnt % Sg;
+                const uint32_t st = ring + s * a.sd.bytes;
+                const int k0 = c * a.sd.chunk, steps = min(a.sd.chunk, m.K - k0) / F::kStep;
+                bool waited = false;
+                uint32_t sc0 = 0, sc1 = 0;
+                if (FMT != kBf16) {
+                    sc0 = scale_addr<FMT>(a.sd, m, u, dual, g, c, st);
+                    sc1 = scale_addr<FMT>(a.sd, m, u, dual, g + 8, c, st);
+                }
+                for (int s0 = gw; s0 < steps || !waited; s0 += kGw * kAhead) {
+                    uint4 b[kAhead][NT][kB];
+                    if (!from_x) {
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                if (s0 + i * kGw < steps && n < ntn) {
+                                    const uint16_t* p = hp[n] + k0 + (s0 + i * kGw) * F::kStep + t4 * (F::kStep / 4);
+#pragma unroll
+                                    for (int q = 0; q < kB; ++q) b[i][n][q] = __ldcg(reinterpret_cast<const uint4*>(p) + q);
+                                }
+                    }
+                    if (!waited) {
+                        waited = true;
+                        if (!dead) {
+                            const bool got = mbar_wait(&full[s], (uint32_t)((cnt / Sg) & 1), s_abort, a.wait_limit);
+                            if (!__all_sync(0xffffffffu, got)) {
+                                dead = true;
+                                if (lane == 0) report_error(a.err, kErrWaitExpired);
+                                *s_abort = 1;
+                            }
+                        }
+                    }
+                    if (dead) break;
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        const int si = s0 + i * kGw;
+                        if (si >= steps) break;
+                        if (from_x) {
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                if (n < ntn) {
+                                    const uint32_t p = xp[n] + (k0 + si * F::kStep) * 2 + t4 * (F::kStep / 2);
+#pragma unroll
+                                    for (int q = 0; q < kB; ++q) b[i][n][q] = lds128(p + 16 * q);
+                                }
+                        }
+                        step<FMT, NT>(a.sd, st, si, sc0, sc1, b[i], ntn, acc);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[s]);
+            }
+        };
+
+        // ---- up projections
+        auto up = [&](const WMat& m, const Unit& u, uint16_t* hbase, int I, float limit) {
+            const uint32_t mask = s_mask[u.e];
+            const int ncol = __popc(mask), ntn = (ncol + 7) / 8;
+            float acc[NT][4];
+            uint32_t xp[NT];
+            const uint16_t* hp[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+                xp[n] = xs + col_token(mask, ncol, n * 8 + g) * xstride;
+                hp[n] = nullptr;
+            }
+            run_unit(m, u, DUAL, true, hp, xp, ntn, acc);
+            // the group's four k shares meet in shared memory
+            float* r = red + rbuf * (L::kRedBuf / 4);
+            rbuf ^= 1;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                if (n < ntn) {
+                    float* p = r + (gw * kRows + g) * TT + n * 8 + 2 * t4;
+                    *reinterpret_cast<float2*>(p) = make_float2(acc[n][0], acc[n][1]);
+                    *reinterpret_cast<float2*>(p + 8 * TT) = make_float2(acc[n][2], acc[n][3]);
+                }
+            named_bar(1 + grp, kGw * 32);
+            const float gl = FMT == kNvfp4 ? __ldg(m.glob + (u.e == a.E ? 0 : u.e)) : 1.0f;
+            for (int i = gt; i < kFeat * ncol; i += kGw * 32) {
+                const int f = i % kFeat, c = i / kFeat;
+                if (f >= u.n || dead) continue;
+                float v = 0.0f, w = 0.0f;
+#pragma unroll
+                for (int q = 0; q < kGw; ++q) {
+                    v += r[(q * kRows + f) * TT + c];
+                    if (DUAL) w += r[(q * kRows + 8 + f) * TT + c];
+                }
+                if (FMT == kNvfp4) {
+                    v *= gl;
+                    w *= gl;
+                }
+                if (DUAL) {
+                    clamp_swiglu(v, w, limit);
+                    v = act_swiglu(v, w);
+                } else {
+                    v = act_relu2(v);
+                }
+                const int t = nth_bit(mask, c);
+                const size_t row = u.e == a.E ? t : (size_t)t * a.k + s_slot[t * 256 + u.e];
+                const int pos = u.f0 + f;
+                // the activation is rounded once to bf16, the down products' operand type
+                __stcg(hbase + row * I + (FMT == kAffine ? affine_pos(pos) : pos), f2bf16(v));
+            }
+        };
+        for (int i = grp; i < s_units; i += kGroups) up(a.S1, shared_up(i), a.hs, a.Is, a.limit_s);
+        const long long Fr = (long long)nact * a.I, f1 = (cta + 1) * Fr / G;
+        int i_up = 0;
+        for (long long f = cta * Fr / G; f < f1; ++i_up) {
+            Unit u;
+            f = routed_up(f, f1, u);
+            if (i_up % kGroups == grp) up(a.W1, u, a.h, a.I, a.limit);
+        }
+        // ---- every h is written
+        named_bar(5, kCThreads);
+        target += G;
+        if (tid == 0) {
+            arrive();
+            grid_wait();
+        }
+        named_bar(5, kCThreads);
+        if (*s_abort) dead = true;
+
+        // ---- down projections
+        const int nd = nact + (a.Is > 0);
+        float* yw = s_red + warp * kRows * TT;                  // this warp's sums [row][token]
+        float* ysw = s_ys + gw * kRows * TT;
+        for (int tile = 0; tile < ytiles; ++tile) {
+            for (int i = lane; i < kRows * TT; i += 32) yw[i] = 0.0f;
+            for (int li = 0; li < nd; ++li) {
+                const Unit u = down_unit(tile, li, nact);
+                const bool routed = li < nact;
+                const WMat& m = routed ? a.W2 : a.S2;
+                if ((tile * nd + li) % kGroups != grp) continue;
+                const uint32_t mask = s_mask[u.e];
+                const int ncol = __popc(mask), ntn = (ncol + 7) / 8;
+                float acc[NT][4];
+                uint32_t xp[NT];
+                const uint16_t* hp[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+                    xp[n] = 0;
+                    const int t = col_token(mask, ncol, n * 8 + g);
+                    hp[n] = routed ? a.h + ((size_t)t * a.k + s_slot[t * 256 + u.e]) * a.I : a.hs + (size_t)t * a.Is;
+                }
+                run_unit(m, u, false, false, hp, xp, ntn, acc);
+                const float gl = FMT == kNvfp4 ? __ldg(m.glob + (routed ? u.e : 0)) : 1.0f;
+                __syncwarp();
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int c = n * 8 + 2 * t4 + i;
+                        if (c < ncol) {
+                            const int t = nth_bit(mask, c);
+                            if (routed) {
+                                const float w = s_wt[t * kMaxK + s_slot[t * 256 + u.e]] * gl;
+                                yw[g * TT + t] += w * acc[n][i];
+                                yw[(g + 8) * TT + t] += w * acc[n][2 + i];
+                            } else {
+                                ysw[g * TT + t] = gl * acc[n][i];
+                                ysw[(g + 8) * TT + t] = gl * acc[n][2 + i];
+                            }
+                        }
+                    }
+                __syncwarp();
+            }
+            named_bar(5, kCThreads);
+            const Unit u = down_unit(tile, nact, nact);
+            for (int i = tid; i < kRows * TT; i += kCThreads) {
+                const int r = i % kRows, t = i / kRows;
+                if (r >= u.n || t >= a.T || dead) continue;
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kCw; ++w) v += s_red[(w * kRows + r) * TT + t];
+                v *= a.out_scale;               // once, on the finished sum
+                if (a.Is > 0) {
+#pragma unroll
+                    for (int w = 0; w < kGw; ++w) v += s_ys[(w * kRows + r) * TT + t];
+                }
+                const size_t o = (size_t)t * a.H + u.f0 + r;
+                if (a.residual) v += bf16f(a.residual[o]);
+                a.y[o] = f2bf16(v);
+            }
+            named_bar(5, kCThreads);
+        }
+    }
+    __syncthreads();
+    // the last CTA out leaves the counters at zero for the next call
+    if (tid == 0) {
+        __threadfence();
+        if (atomicAdd(a.sync + 1, 1u) == (uint32_t)G - 1) {
+            a.sync[0] = 0;
+            a.sync[1] = 0;
+        }
+    }
+}
+
+template <int FMT, int NT, bool DUAL>
+cudaError_t run(DecodeArgs& a, cudaStream_t s) {
+    const DeviceInfo& di = device_info();
+    using F = Fmt<FMT>;
+    const size_t fixed = Layout<NT>::kX + (((size_t)a.T * (a.H * 2 + F::kXPad) + 127) & ~size_t(127));
+    // 1 KB of each row a stage, or 512 bytes where the token rows leave room
+    // for less than two slots per group
+    const size_t room = fixed < (size_t)di.max_smem_optin ? di.max_smem_optin - fixed : 0;
+    a.sd = F::dims(FMT == kBf16 ? 512 : 2048);
+    if (room < (size_t)2 * kGroups * a.sd.bytes) a.sd = F::dims(FMT == kBf16 ? 256 : 1024);
+    a.stages = (int)std::min<size_t>(kMaxStages, room / a.sd.bytes) / kGroups;
+    if (a.stages < 1) return cudaErrorNotSupported;
+    const size_t smem = fixed + (size_t)kGroups * a.stages * a.sd.bytes;
+    auto kern = k_decode<FMT, NT, DUAL>;
+    cudaError_t e = ensure_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(di.sm_count);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int FMT>
+cudaError_t run_fmt(DecodeArgs& a, bool dual, cudaStream_t s) {
+    if (a.T <= 8) return dual ? run<FMT, 1, true>(a, s) : run<FMT, 1, false>(a, s);
+    return dual ? run<FMT, 2, true>(a, s) : run<FMT, 2, false>(a, s);
+}
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+struct DecodeWs {
+    size_t sync, lg, h, hs, total;
+};
+
+DecodeWs ws_layout(const moe_dims* d, int Is) {
+    DecodeWs L{};
+    L.sync = 0;
+    size_t off = 256;
+    L.lg = off;
+    off = align256(off + (size_t)d->T * d->E * 8);
+    L.h = off;
+    off = align256(off + (size_t)d->T * d->k * d->I * 2);
+    L.hs = off;
+    L.total = align256(off + (size_t)d->T * Is * 2);
+    return L;
+}
+
+moe_status refuse(moe_status st, const char* msg) {
+    set_last_error(msg);
+    return st;
+}
+
+// Sizes of moe_decode: moe_dims' limits, few tokens, and token rows that fit
+// shared memory beside the weight ring.
+moe_status check_sizes(const moe_dims* d, int Is) {
+    moe_status st = validate_dims(d);
+    if (st != MOE_OK) return st;
+    if (d->T > MOE_DECODE_MAX_T) return refuse(MOE_ERR_SHAPE, "moe_decode: T > 16 (use moe_forward)");
+    if ((long long)d->T * d->H > 65536) return refuse(MOE_ERR_SHAPE, "moe_decode: T * H > 65536 (use moe_forward)");
+    if (Is < 0 || Is > 16384 || Is % 64)
+        return refuse(MOE_ERR_SHAPE, "moe_decode: Is must be 0 or a multiple of 64 up to 16384");
+    return MOE_OK;
+}
+
+WMat mat(const void* w, const void* scale, const void* bias, const float* glob, int rows, int K) {
+    return WMat{static_cast<const unsigned char*>(w), static_cast<const unsigned char*>(scale),
+                static_cast<const unsigned char*>(bias), glob, rows, K};
+}
+
+bool misaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_decode_workspace_bytes(const moe_dims* d, int32_t Is) {
+    return check_sizes(d, Is) == MOE_OK ? ws_layout(d, Is).total : 0;
+}
+
+moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void* x, const float* logits,
+                      const void* residual, int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes,
+                      moe_stream_t stream) {
+    if (!L) return refuse(MOE_ERR_NULL, "layer is NULL");
+    moe_status st = check_sizes(d, L->Is);
+    if (st != MOE_OK) return st;
+    if (L->router.score != MOE_SCORE_SIGMOID && L->router.score != MOE_SCORE_SOFTMAX)
+        return refuse(MOE_ERR_UNSUPPORTED, "router score");
+    if (L->router.norm_topk != 0 && L->router.norm_topk != 1) return refuse(MOE_ERR_UNSUPPORTED, "norm_topk");
+    if (d->T == 0) return set_last_launch_count(0), MOE_OK;   // empty batch: nothing to do
+    if (!x || !y) return refuse(MOE_ERR_NULL, "x or y is NULL");
+    if (!topk_idx || !topk_w) return refuse(MOE_ERR_NULL, "topk_idx or topk_w is NULL");
+    if (!logits && !L->w_router) return refuse(MOE_ERR_NULL, "w_router is NULL (routing from x)");
+    if (misaligned(x, 16) || misaligned(y, 16)) return refuse(MOE_ERR_ALIGN, "x or y not 16-byte aligned");
+    if (misaligned(residual, 16)) return refuse(MOE_ERR_ALIGN, "residual not 16-byte aligned");
+    if (!logits && misaligned(L->w_router, 16)) return refuse(MOE_ERR_ALIGN, "w_router not 16-byte aligned");
+    if (misaligned(logits, 4) || misaligned(L->expert_bias, 4) || misaligned(topk_idx, 4) || misaligned(topk_w, 4))
+        return refuse(MOE_ERR_ALIGN, "logits, expert_bias, topk_idx or topk_w not 4-byte aligned");
+    if ((st = validate_weights(&L->W)) != MOE_OK) return st;
+    if (L->Is > 0) {
+        if ((st = validate_weights(&L->Ws)) != MOE_OK) return st;
+        if (L->Ws.fmt != L->W.fmt || L->Ws.act != L->W.act)
+            return refuse(MOE_ERR_UNSUPPORTED, "the shared expert's format or activation differs from the routed experts'");
+    }
+    const DecodeWs wl = ws_layout(d, L->Is);
+    if (!ws) return refuse(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if (misaligned(ws, 256)) return refuse(MOE_ERR_ALIGN, "workspace not 256-byte aligned");
+    if (ws_bytes < wl.total) return refuse(MOE_ERR_WORKSPACE, "workspace smaller than moe_decode_workspace_bytes()");
+    char* b = static_cast<char*>(ws);
+    const bool dual = L->W.act == MOE_ACT_SWIGLU;
+    DecodeArgs a{};
+    a.x = static_cast<const uint16_t*>(x);
+    a.logits = logits;
+    a.w_router = L->w_router;
+    a.ebias = L->expert_bias;
+    a.residual = static_cast<const uint16_t*>(residual);
+    a.W1 = mat(L->W.w1, L->W.w1_scale, L->W.w1_bias, L->W.w1_global, dual ? 2 * d->I : d->I, d->H);
+    a.W2 = mat(L->W.w2, L->W.w2_scale, L->W.w2_bias, L->W.w2_global, d->H, d->I);
+    if (L->Is > 0) {
+        a.S1 = mat(L->Ws.w1, L->Ws.w1_scale, L->Ws.w1_bias, L->Ws.w1_global, dual ? 2 * L->Is : L->Is, d->H);
+        a.S2 = mat(L->Ws.w2, L->Ws.w2_scale, L->Ws.w2_bias, L->Ws.w2_global, d->H, L->Is);
+        a.limit_s = L->Ws.swiglu_limit;
+    }
+    a.T = d->T;
+    a.H = d->H;
+    a.E = d->E;
+    a.k = d->k;
+    a.I = d->I;
+    a.Is = L->Is;
+    a.eps = L->eps;
+    a.scale = L->router_scale;
+    a.out_scale = L->out_scale;
+    a.limit = L->W.swiglu_limit;
+    a.softmax = L->router.score == MOE_SCORE_SOFTMAX;
+    a.no_norm = L->router.norm_topk == 0;
+    a.idx = topk_idx;
+    a.w = topk_w;
+    a.y = static_cast<uint16_t*>(y);
+    a.sync = reinterpret_cast<uint32_t*>(b + wl.sync);
+    a.lg = reinterpret_cast<double*>(b + wl.lg);
+    a.h = reinterpret_cast<uint16_t*>(b + wl.h);
+    a.hs = reinterpret_cast<uint16_t*>(b + wl.hs);
+    a.wait_limit = sm100::kWaitLimit;
+    a.err = device_info().err_word;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = L->W.fmt == MOE_W_BF16          ? run_fmt<kBf16>(a, dual, s)
+                          : L->W.fmt == MOE_W_AFFINE4_G64 ? run_fmt<kAffine>(a, dual, s)
+                                                          : run_fmt<kNvfp4>(a, dual, s);
+    if (e == cudaErrorNotSupported) return refuse(MOE_ERR_UNSUPPORTED, "moe_decode: shared memory of this device");
+    if (e != cudaSuccess) {
+        set_last_error(cudaGetErrorString(e));
+        return MOE_ERR_CUDA;
+    }
+    set_last_launch_count(1);
+    return MOE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,273 @@
+"""The few-token MoE layer (moe_decode) against the float64 oracle.
+
+Tolerances.  A rounding to bf16 is off by at most u = 2^-8 of the value.  The
+kernel rounds twice: every activation h to bf16, and y.  So per element
+    |y_gpu - y| <= u |y| + u A (1 + s),   A = out_scale sum_j |w_j| sum_i |W2| |h| + the shared expert's,
+where s covers the fp32 sums: a pre-activation is off by at most n 2^-24 of its
+sum of absolute products (n = H terms), which in units of u is below 1 for the
+sizes here (H <= 4096: 4096 * 2^-24 = u / 16 of that sum; |act'| of it enters h).
+s = 1 is used.  The norm-wise gate: errors of independent roundings, each at
+most u relative, leave at most sqrt(2) u of y's norm when nothing cancels
+systematically; 2 u is the gate.  Picks must be the oracle's; weights are
+float64 rounded once to fp32 (2^-24; 2^-23 allows for exp's own last bit).
+"""
+import dataclasses
+
+import numpy as np
+import pytest
+
+import oracle as O
+from sigmoid_top_routing_b200 import inputs as G
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def api():
+    from sigmoid_top_routing_b200 import build
+    build.build(quiet=True)
+    from sigmoid_top_routing_b200 import api as A
+    A.load()
+    return A
+
+
+_CACHE = {}
+
+
+def inputs_of(wl):
+    if wl not in _CACHE:
+        _CACHE.clear()
+        _CACHE[wl] = G.make_inputs(wl)
+    return _CACHE[wl]
+
+
+def residual_of(wl):
+    r = np.random.default_rng(7).standard_normal((wl.T, wl.H)).astype(np.float32)
+    return G.f32_to_bf16_bits(r)
+
+
+def make_layer(api, inp, **over):
+    from sigmoid_top_routing_b200.device_inputs import shared_to_device, to_device
+    wl = inp.wl
+    D = to_device(inp)
+    kw = dict(E=wl.E, k=wl.k, I=wl.I, Ws=shared_to_device(inp), Is=wl.shared_I, eps=wl.eps,
+              router_scale=wl.router_scale, out_scale=wl.out_scale, score=wl.score, norm_topk=wl.norm_topk,
+              max_tokens=wl.T)
+    kw.update(over)
+    layer = api.DecodeLayer(D.W, D.w_router, D.expert_bias, **kw)
+    layer.ws[256:].fill_(0xFF)                       # only the counters need zeros
+    return D, layer
+
+
+def bits(t):
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+def magnitude(inp, r):
+    """A of the module docstring, for every element of y."""
+    wl = inp.wl
+    x = O.bf16_to_f64(inp.x_bits)
+    A = np.zeros((wl.T, wl.H))
+    from oracle.moe_oracle import _act, _expert_w, _shared_w
+    for e in np.unique(r["idx"]):
+        W1, W2 = _expert_w(inp, "w1", int(e)), _expert_w(inp, "w2", int(e))
+        for t, j in zip(*np.nonzero(r["idx"] == e)):
+            h = _act(x[t:t + 1] @ W1.T, wl.act, wl.I, wl.swiglu_limit)
+            A[t] += abs(r["w"][t, j]) * (np.abs(h) @ np.abs(W2).T)[0]
+    A *= abs(wl.out_scale)
+    if wl.shared_I:
+        h = _act(x @ _shared_w(inp, "w1").T, wl.act, wl.shared_I, wl.swiglu_limit)
+        A += np.abs(h) @ np.abs(_shared_w(inp, "w2")).T
+    return A
+
+
+def compare(inp, y, idx, w, residual=None, logits=None):
+    r = O.moe_block(inp, use_logits=logits)
+    nan = np.isnan(r["c"]).all(axis=1)
+    assert np.array_equal(idx, r["idx"])
+    np.testing.assert_allclose(w[~nan], r["w"][~nan], rtol=2.0 ** -23, atol=0)
+    want = r["y"] + (O.bf16_to_f64(residual) if residual is not None else 0.0)
+    got = O.bf16_to_f64(y)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    ok = ~np.isnan(want).any(axis=1)
+    if ok.any():
+        err = np.abs(got - want)[ok]
+        tol = U * np.abs(want) + 2 * U * magnitude(inp, r)
+        assert (err <= tol[ok] + 1e-30).all(), (err / (tol[ok] + 1e-30)).max()
+        # the norm of what the experts add, not of the residual
+        assert np.linalg.norm(err) <= 2 * U * np.linalg.norm(want[ok])
+
+
+def run_and_compare(api, wl, residual=True, logits=None):
+    inp = inputs_of(wl)
+    D, layer = make_layer(api, inp)
+    res = residual_of(wl) if residual else None
+    from sigmoid_top_routing_b200.device_inputs import bf16_tensor
+    rt = bf16_tensor(res, "cuda") if residual else None
+    # outputs inside guard rows: nothing outside them is written
+    yb = torch.full((wl.T + 2, wl.H), -1, dtype=torch.int16, device="cuda")
+    ib = torch.full((wl.T + 2, wl.k), -1, dtype=torch.int32, device="cuda")
+    wb = torch.full((wl.T + 2, wl.k), -1, dtype=torch.int32, device="cuda")
+    y = yb.view(torch.bfloat16)[1:-1]
+    lg = None if logits is None else torch.from_numpy(logits).cuda()
+    layer(D.x, residual=rt, logits=lg, y=y, topk_idx=ib[1:-1], topk_w=wb.view(torch.float32)[1:-1])
+    torch.cuda.synchronize()
+    assert api.moe_device_error() == 0
+    assert api.moe_last_launch_count() == 1
+    for b in (yb, ib, wb):
+        assert (b[0] == -1).all() and (b[-1] == -1).all()
+    assert (layer.ws[:256] == 0).all()
+    compare(inp, bits(y), ib[1:-1].cpu().numpy(), wb.view(torch.float32)[1:-1].cpu().numpy(), res, logits)
+
+
+W = G.Workload
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "affine4", "nvfp4"])
+@pytest.mark.parametrize("wl", [
+    W("one", T=1, H=64, E=1, k=1, I=64),                                       # the smallest sizes
+    W("tiny", T=3, H=256, E=8, k=2, I=128, swiglu_limit=1.0),
+    W("relu2", T=5, H=320, E=16, k=6, I=192, act="relu2", out_scale=2.5),      # 3 groups: odd scale rows
+    W("shared", T=8, H=448, E=12, k=3, I=320, shared_I=576, out_scale=0.5),
+    W("wide", T=9, H=2176, E=6, k=2, I=192, shared_I=64),                      # 9 columns; 4-bit rows in 2 chunks
+    W("long", T=2, H=192, E=4, k=2, I=4160, act="relu2"),                      # long down rows, odd groups
+    W("many", T=16, H=128, E=256, k=32, I=64),                                 # the most experts and picks
+    W("softmax", T=13, H=512, E=40, k=5, I=256, score="softmax", norm_topk=False),
+], ids=lambda w: w.name)
+def test_parity(api, wl, fmt):
+    run_and_compare(api, dataclasses.replace(wl, fmt=fmt, name=f"{wl.name}_{fmt}"))
+
+
+def test_limits_of_the_sizes(api):
+    run_and_compare(api, W("t16", T=16, H=4096, E=4, k=2, I=64))               # T * H = 65536
+    run_and_compare(api, W("h16384", T=4, H=16384, E=3, k=1, I=64), residual=False)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "affine4", "nvfp4"])
+def test_one_expert_takes_every_token(api, fmt):
+    """Two column blocks of one expert, the others empty."""
+    wl = W("hot", T=16, H=256, E=8, k=1, I=192, fmt=fmt)
+    lg = np.full((16, 8), -4.0, dtype=np.float32)
+    lg[:, 3] = 4.0
+    run_and_compare(api, wl, logits=lg)
+
+
+def test_ties_take_the_lower_expert(api):
+    wl = W("ties", T=4, H=128, E=40, k=7, I=64, score="softmax")
+    lg = np.zeros((4, 40), dtype=np.float32)
+    lg[1, 35:] = 1.0
+    lg[2, ::2] = -0.0
+    inp = inputs_of(wl)
+    inp.expert_bias[:] = 0.0
+    run_and_compare(api, wl, logits=lg)
+    _CACHE.clear()
+
+
+def test_nan_and_infinite_rows(api):
+    """A row of NaN picks 0..k-1 and its output is NaN; its neighbours do not notice."""
+    wl = W("nan", T=6, H=256, E=8, k=3, I=128, nan_rows=2)
+    run_and_compare(api, wl)
+    wl = dataclasses.replace(wl, name="inf", nan_rows=0)
+    lg = np.random.default_rng(3).standard_normal((6, 8)).astype(np.float32)
+    lg[1] = np.nan
+    lg[2, 4] = np.nan
+    lg[3, 5] = np.inf
+    lg[4, :] = -np.inf
+    run_and_compare(api, wl, logits=lg)
+
+
+@pytest.mark.parametrize("alias", ["residual", "x"])
+def test_output_in_place(api, alias):
+    wl = W("alias", T=7, H=320, E=8, k=2, I=128, shared_I=64)
+    inp = inputs_of(wl)
+    D, layer = make_layer(api, inp)
+    from sigmoid_top_routing_b200.device_inputs import bf16_tensor
+    r = bf16_tensor(residual_of(wl), "cuda")
+    want, idx, w = layer(D.x, residual=r)
+    dst = r if alias == "residual" else D.x
+    got, idx2, w2 = layer(D.x, residual=r, y=dst)
+    assert torch.equal(got, want) and torch.equal(idx, idx2) and torch.equal(w, w2)
+    assert got.data_ptr() == dst.data_ptr()
+
+
+def test_empty_batch(api):
+    wl = W("empty", T=2, H=64, E=2, k=1, I=64)
+    D, layer = make_layer(api, inputs_of(wl))
+    y, idx, w = layer(D.x[:0])
+    assert y.shape == (0, 64) and idx.shape == (0, 1) and api.moe_last_launch_count() == 0
+
+
+def test_fewer_tokens_than_max_and_repeated_calls(api):
+    """One workspace serves every T up to max_tokens, call after call, with the same bits."""
+    wl = W("rep", T=16, H=512, E=16, k=4, I=256, shared_I=128)
+    D, layer = make_layer(api, inputs_of(wl))
+    first = {T: layer(D.x[:T]) for T in (16, 1, 8, 9, 3)}
+    for T in (3, 9, 8, 1, 16):
+        for a, b in zip(first[T], layer(D.x[:T])):
+            assert torch.equal(a, b)
+
+
+def test_graph_and_side_stream(api):
+    wl = W("graph", T=4, H=512, E=16, k=4, I=256)
+    D, layer = make_layer(api, inputs_of(wl))
+    x = D.x.clone()
+    want = [t.clone() for t in layer(x)]
+    x2 = (D.x.float() * 0.5).bfloat16()
+    want2 = [t.clone() for t in layer(x2)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = layer(x)
+    torch.cuda.current_stream().wait_stream(s)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = layer(x)
+        out2 = layer(out[0], residual=x)
+    for src, ref in ((D.x, want), (x2, want2), (D.x, want)):
+        x.copy_(src)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(ref, out):
+            assert torch.equal(a, b)
+        for a, b in zip(layer(ref[0], residual=src), out2):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", ["lfm2_decode_t8", "affine4_t8", "nvfp4_t1", "affine4_t1"])
+def test_agrees_with_moe_forward(api, name):
+    """The layer and the multi-kernel block: same picks, outputs within both sides' roundings."""
+    wl = G.WORKLOADS[name]
+    inp = inputs_of(wl)
+    D, layer = make_layer(api, inp)
+    y, idx, w = layer(D.x)
+    y2, idx2, w2, _ = api.moe_forward(D.x, D.W, D.w_router, D.expert_bias, E=wl.E, k=wl.k, I=wl.I, eps=wl.eps,
+                                      router_scale=wl.router_scale, out_scale=wl.out_scale)
+    assert torch.equal(idx, idx2)
+    a, b = y.float(), y2.float()
+    assert (a - b).norm() <= 4 * U * b.norm()
+    compare(inp, bits(y), idx.cpu().numpy(), w.cpu().numpy())
+
+
+def test_python_refusals(api):
+    wl = W("refuse", T=4, H=128, E=4, k=2, I=64)
+    D, layer = make_layer(api, inputs_of(wl))
+    with pytest.raises(ValueError):
+        layer(torch.cat([D.x, D.x]))                             # more than max_tokens
+    with pytest.raises(ValueError):
+        layer(D.x.float())
+    with pytest.raises(ValueError):
+        layer(D.x[:, ::2])
+    with pytest.raises(ValueError):
+        layer(D.x, residual=D.x[:2])
+    with pytest.raises(ValueError):
+        layer(D.x.cpu())
+    with pytest.raises(ValueError):
+        api.DecodeLayer(D.W, D.w_router, D.expert_bias, E=4, k=2, I=128)
+    with pytest.raises(ValueError):
+        api.DecodeLayer(D.W, D.w_router, D.expert_bias, E=4, k=2, I=64, max_tokens=17)
