@@ -47,7 +47,7 @@ constexpr int kGroups = 4;                      // consumer groups, each on a ti
 constexpr int kGw = 4;                          // warps of a group: they share a tile's k
 constexpr int kCw = kGroups * kGw;              // consumer warps
 constexpr int kCThreads = kCw * 32;
-constexpr int kThreads = kCThreads + 32;        // + the producer warp
+constexpr int kThreads = kCThreads + kGroups * 32;   // + a producer warp per group
 constexpr int kMaxE = 257;                      // 256 experts and the shared one
 constexpr int kMaxK = 32;
 constexpr int kMaxStages = 16;
@@ -96,9 +96,9 @@ struct Layout {                                 // shared memory (byte offsets)
     static constexpr int kRed = kBar + 2 * kMaxStages * 8;            // group sums; later y sums per warp
     static constexpr int kRedBuf = kGw * kRows * kTok * 4;            // one buffer of one group
     static constexpr int kRedBytes = kGroups * 2 * kRedBuf;
-    static constexpr int kYs = kRed + kRedBytes;                      // shared expert's y sums, one per warp of a group
-    static constexpr int kX = (kYs + kGw * kRows * kTok * 4 + 127) & ~127;
-    static_assert(kCw * kRows * kTok * 4 <= kRedBytes, "y sums fit the group-sum buffers");
+    static constexpr int kYs = kRed + kRedBytes / 2;                  // the shared expert's y sums per warp
+    static constexpr int kX = (kRed + kRedBytes + 127) & ~127;
+    static_assert(2 * kCw * kRows * kTok * 4 <= kRedBytes, "both y sums fit the group-sum buffers");
 };
 
 MOE_DEV uint64_t key64(double c) {              // order of c; NaN lowest (1), -0 == +0
@@ -198,6 +198,9 @@ struct Unit {
     int f0;                                     // first feature (up) or row of y (down)
     size_t row0, row1;                          // first weight row; of the up half when dual
 };
+
+// Start of part i of n equal parts of v (v * (i + 1) must fit 32 bits).
+MOE_DEV int part(int v, int i, int n) { return (int)((uint32_t)v * (uint32_t)i / (uint32_t)n); }
 
 MOE_DEV int chunks_of(int K, const StageDims& sd) { return (K + sd.chunk - 1) / sd.chunk; }
 
@@ -366,125 +369,111 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
     }
     __syncthreads();
 
-    // This CTA's parts: features of the shared expert, features of the routed
-    // experts' list (once it is known), rows of y.
-    const int sf0 = (int)((long long)cta * a.Is / G), sf1 = (int)((long long)(cta + 1) * a.Is / G);
-    const int yr0 = (int)((long long)cta * a.H / G), yr1 = (int)((long long)(cta + 1) * a.H / G);
+    const int grp = warp < kCw ? warp / kGw : warp - kCw;
+    const int ring0 = grp * Sg;                 // first ring slot of this warp's group
+
+    // Work of this group: equal parts, over all groups of the grid, of the
+    // shared expert's features and of the routed experts' list (once it is known).
+    const int wk = cta * kGroups + grp, nwk = G * kGroups;
+    const int sf0 = part(a.Is, wk, nwk), sf1 = part(a.Is, wk + 1, nwk);
+    // This CTA's rows of y, in tiles of at most 16; each tile's list of
+    // (expert, chunk of k) is dealt out to the groups in equal parts.
+    const int yr0 = part(a.H, cta, G), yr1 = part(a.H, cta + 1, G);
     const int ytiles = (yr1 - yr0 + kRows - 1) / kRows;
-    const int up_chunks = chunks_of(a.H, a.sd);
-    const int s_units = (sf1 - sf0 + kFeat - 1) / kFeat;
+    const int up_chunks = chunks_of(a.H, a.sd), i_chunks = chunks_of(a.I, a.sd), is_chunks = chunks_of(a.Is, a.sd);
 
-    auto shared_up = [&](int i) {               // i-th tile of the shared expert's features
-        Unit u;
-        u.e = a.E;
-        u.f0 = sf0 + i * kFeat;
-        u.n = min(kFeat, sf1 - u.f0);
-        u.row0 = u.f0;
-        u.row1 = (size_t)a.Is + u.f0;
-        return u;
+    auto for_shared_up = [&](auto&& f) {        // f(unit) for the group's tiles of the shared expert
+        for (int p = sf0; p < sf1; p += kFeat) {
+            const Unit u{a.E, min(kFeat, sf1 - p), p, (size_t)p, (size_t)a.Is + p};
+            if (!f(u)) return;
+        }
     };
-    auto routed_up = [&](long long f, long long f1, Unit& u) {   // tile at list position f; returns the next f
-        const int li = (int)(f / a.I), off = (int)(f - (long long)li * a.I);
-        u.e = s_list[li];
-        u.f0 = off;
-        u.n = (int)min((long long)min(kFeat, a.I - off), f1 - f);
-        u.row0 = (size_t)u.e * a.W1.rows + off;
-        u.row1 = u.row0 + a.I;
-        return f + u.n;
+    auto for_routed_up = [&](int nact, auto&& f) {
+        int p = part(nact * a.I, wk, nwk);
+        const int end = part(nact * a.I, wk + 1, nwk);
+        int li = p / a.I, off = p - li * a.I;
+        while (p < end) {
+            const int e = s_list[li], n = min(min(kFeat, a.I - off), end - p);
+            const size_t r = (size_t)e * a.W1.rows + off;
+            if (!f(Unit{e, n, off, r, r + a.I})) return;
+            p += n;
+            off += n;
+            if (off == a.I) {
+                off = 0;
+                ++li;
+            }
+        }
     };
-    auto down_unit = [&](int tile, int li, int nact) {           // li == nact: the shared expert
-        Unit u;
-        const int b = (int)((long long)tile * (yr1 - yr0) / ytiles), e = (int)((long long)(tile + 1) * (yr1 - yr0) / ytiles);
-        u.e = li < nact ? s_list[li] : a.E;
-        u.f0 = yr0 + b;
-        u.n = e - b;
-        u.row0 = (li < nact ? (size_t)u.e * a.H : 0) + u.f0;
-        u.row1 = u.row0;
-        return u;
+    // f(unit, first chunk, end chunk) for the group's runs of chunks of one row tile
+    auto for_down = [&](int nact, int tile, auto&& f) {
+        const int r0 = yr0 + part(yr1 - yr0, tile, ytiles), r1 = yr0 + part(yr1 - yr0, tile + 1, ytiles);
+        const int total = nact * i_chunks + is_chunks;
+        int q = part(total, grp, kGroups);
+        const int end = part(total, grp + 1, kGroups);
+        while (q < end) {
+            const int li = min(q / i_chunks, nact);
+            const bool routed = li < nact;
+            const int c0 = q - li * i_chunks, c1 = min(routed ? i_chunks : is_chunks, c0 + end - q);
+            const int e = routed ? s_list[li] : a.E;
+            const size_t r = (routed ? (size_t)e * a.H : 0) + r0;
+            if (!f(Unit{e, r1 - r0, r0, r, r}, c0, c1)) return;
+            q += c1 - c0;
+        }
     };
 
-    if (warp == kCw) {
-        // -------------------------------------------------------- producer
+    if (warp >= kCw) {
+        // -------------------------------------------------------- producer of one group
         const uint64_t pol = policy_evict_first();
-        int cnt[kGroups] = {};                  // stages issued, per group
+        int slot = 0, fills = 0;                // next ring slot; stages issued
+        uint32_t ph = 1;                        // parity of the slot's last release (fresh: passes)
         bool ok = true;
-        auto push = [&](int gr, const WMat& m, const Unit& u, bool dual, int c) {
-            const int q = cnt[gr], s = gr * Sg + q % Sg;
-            if (q >= Sg) {
-                const bool got = mbar_wait(&empty[s], (uint32_t)((q / Sg - 1) & 1), s_abort, a.wait_limit);
-                if (!__all_sync(0xffffffffu, got)) ok = false;
+        auto push = [&](const WMat& m, const Unit& u, bool dual, int c) {
+            const int s = ring0 + slot;
+            const bool got = mbar_wait(&empty[s], ph, s_abort, a.wait_limit);
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                return;
             }
-            if (!ok) return;
             issue_stage<FMT>(a.sd, m, u, dual, c, ring + s * a.sd.bytes, &full[s], pol);
-            ++cnt[gr];
-        };
-        // Units go to the groups in turn; the stages of kGroups units are
-        // issued chunk by chunk, so all groups' slots fill at one rate.
-        // shared(first, only_free): the shared expert's stages from number
-        // `first` on; with only_free it stops where it would wait.
-        auto shared = [&](int first, bool only_free) {
-            int q = 0;
-            for (int b = 0; b < s_units; b += kGroups)
-                for (int c = 0; c < up_chunks; ++c)
-#pragma unroll
-                    for (int gr = 0; gr < kGroups; ++gr)
-                        if (b + gr < s_units && q++ >= first && ok) {
-                            if (only_free && cnt[gr] >= Sg) return q - 1;
-                            push(gr, a.S1, shared_up(b + gr), DUAL, c);
-                        }
-            return q;
-        };
-        const int pre = shared(0, true);        // needs no routing
-        __syncthreads();                        // routing tables ready
-        shared(pre, false);
-        const int nact = *s_nact;
-        const long long Fr = (long long)nact * a.I;
-        const long long f1 = (cta + 1) * Fr / G;
-        for (long long f = cta * Fr / G; f < f1 && ok;) {
-            Unit u[kGroups];
-            int nu = 0;
-#pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr)
-                if (f < f1) {
-                    f = routed_up(f, f1, u[gr]);
-                    nu = gr + 1;
-                }
-            for (int c = 0; c < up_chunks && ok; ++c)
-#pragma unroll
-                for (int gr = 0; gr < kGroups; ++gr)
-                    if (gr < nu && ok) push(gr, a.W1, u[gr], DUAL, c);
-        }
-        const int nd = nact + (a.Is > 0), i_chunks = chunks_of(a.I, a.sd), is_chunks = chunks_of(a.Is, a.sd);
-        for (int b = 0; b < ytiles * nd && ok; b += kGroups) {
-            Unit u[kGroups];
-            int nch[kGroups], most = 0;
-#pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr) {
-                const int i = b + gr;
-                nch[gr] = 0;
-                if (i < ytiles * nd) {
-                    u[gr] = down_unit(i / nd, i % nd, nact);
-                    nch[gr] = i % nd < nact ? i_chunks : is_chunks;
-                    most = max(most, nch[gr]);
-                }
+            ++fills;
+            if (++slot == Sg) {
+                slot = 0;
+                ph ^= 1;
             }
-            for (int c = 0; c < most && ok; ++c)
-#pragma unroll
-                for (int gr = 0; gr < kGroups; ++gr)
-                    if (c < nch[gr] && ok) push(gr, u[gr].e < a.E ? a.W2 : a.S2, u[gr], false, c);
-        }
+        };
+        // the shared expert's first rows need no routing: fill the free slots with them
+        int pre = 0;
+        for_shared_up([&](const Unit& u) {
+            for (int c = 0; c < up_chunks && pre < Sg; ++c, ++pre) push(a.S1, u, DUAL, c);
+            return pre < Sg;
+        });
+        __syncthreads();                        // routing tables ready
+        int q = 0;
+        for_shared_up([&](const Unit& u) {
+            for (int c = 0; c < up_chunks && ok; ++c)
+                if (q++ >= pre) push(a.S1, u, DUAL, c);
+            return ok;
+        });
+        const int nact = *s_nact;
+        for_routed_up(nact, [&](const Unit& u) {
+            for (int c = 0; c < up_chunks && ok; ++c) push(a.W1, u, DUAL, c);
+            return ok;
+        });
+        for (int tile = 0; tile < ytiles; ++tile)
+            for_down(nact, tile, [&](const Unit& u, int c0, int c1) {
+                for (int c = c0; c < c1 && ok; ++c) push(u.e < a.E ? a.W2 : a.S2, u, false, c);
+                return ok;
+            });
         if (!ok) {
             if (lane == 0) report_error(a.err, kErrWaitExpired);
             *s_abort = 1;
         }
         // every copy issued lands before the CTA can exit
-#pragma unroll
-        for (int gr = 0; gr < kGroups; ++gr)
-            for (int q = max(0, cnt[gr] - Sg); q < cnt[gr]; ++q)
-                mbar_wait(&full[gr * Sg + q % Sg], (uint32_t)((q / Sg) & 1), nullptr, a.wait_limit);
+        for (int i = max(0, fills - Sg); i < fills; ++i)
+            mbar_wait(&full[ring0 + i % Sg], (uint32_t)((i / Sg) & 1), nullptr, a.wait_limit);
     } else {
         // -------------------------------------------------------- consumers
-        const int grp = warp / kGw, gw = warp % kGw, gt = tid % (kGw * 32);
+        const int gw = warp % kGw, gt = tid % (kGw * 32);
         const int g = lane >> 2, t4 = lane & 3;
         bool dead = false;
         uint32_t target = 0;
@@ -573,7 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         }
         __syncthreads();                        // routing tables ready (producer too)
         const int nact = *s_nact;
-        int cnt = 0;                            // stages this group has passed
+        int slot = 0;                           // this group's next ring slot, and its parity
+        uint32_t ph = 0;
         // Columns: token of this lane's operand column per 8-token block, and
         // the row of its activations.
         auto col_token = [&](uint32_t mask, int ncol, int c) { return nth_bit(mask, c < ncol ? c : 0); };
@@ -581,11 +571,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         int rbuf = 0;
 
         // the products of one unit: acc = rows x columns over this warp's share of k
-        auto run_unit = [&](const WMat& m, const Unit& u, bool dual, bool from_x, const uint16_t* (&hp)[NT],
+        auto run_unit = [&](const WMat& m, const Unit& u, int c0, int c1, bool dual, bool from_x, const uint16_t* (&hp)[NT],
                             const uint32_t (&xp)[NT], int ntn, float (&acc)[NT][4]) {
-            const int nch = chunks_of(m.K, a.sd);
-            for (int c = 0; c < nch; ++c, ++cnt) {
-                const int s = grp * Sg + cnt % Sg;
+            for (int c = c0; c < c1; ++c) {
+                const int s = ring0 + slot;
                 const uint32_t st = ring + s * a.sd.bytes;
                 const int k0 = c * a.sd.chunk, steps = min(a.sd.chunk, m.K - k0) / F::kStep;
                 bool waited = false;
@@ -610,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                     if (!waited) {
                         waited = true;
                         if (!dead) {
-                            const bool got = mbar_wait(&full[s], (uint32_t)((cnt / Sg) & 1), s_abort, a.wait_limit);
+                            const bool got = mbar_wait(&full[s], ph, s_abort, a.wait_limit);
                             if (!__all_sync(0xffffffffu, got)) {
                                 dead = true;
                                 if (lane == 0) report_error(a.err, kErrWaitExpired);
@@ -637,6 +626,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[s]);
+                if (++slot == Sg) {
+                    slot = 0;
+                    ph ^= 1;
+                }
             }
         };
 
@@ -653,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 xp[n] = xs + col_token(mask, ncol, n * 8 + g) * xstride;
                 hp[n] = nullptr;
             }
-            run_unit(m, u, DUAL, true, hp, xp, ntn, acc);
+            run_unit(m, u, 0, up_chunks, DUAL, true, hp, xp, ntn, acc);
             // the group's four k shares meet in shared memory
             float* r = red + rbuf * (L::kRedBuf / 4);
             rbuf ^= 1;
@@ -692,14 +685,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 __stcg(hbase + row * I + (FMT == kAffine ? affine_pos(pos) : pos), f2bf16(v));
             }
         };
-        for (int i = grp; i < s_units; i += kGroups) up(a.S1, shared_up(i), a.hs, a.Is, a.limit_s);
-        const long long Fr = (long long)nact * a.I, f1 = (cta + 1) * Fr / G;
-        int i_up = 0;
-        for (long long f = cta * Fr / G; f < f1; ++i_up) {
-            Unit u;
-            f = routed_up(f, f1, u);
-            if (i_up % kGroups == grp) up(a.W1, u, a.h, a.I, a.limit);
-        }
+        for_shared_up([&](const Unit& u) {
+            up(a.S1, u, a.hs, a.Is, a.limit_s);
+            return true;
+        });
+        for_routed_up(nact, [&](const Unit& u) {
+            up(a.W1, u, a.h, a.I, a.limit);
+            return true;
+        });
         // ---- every h is written
         named_bar(5, kCThreads);
         target += G;
@@ -711,16 +704,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         if (*s_abort) dead = true;
 
         // ---- down projections
-        const int nd = nact + (a.Is > 0);
         float* yw = s_red + warp * kRows * TT;                  // this warp's sums [row][token]
-        float* ysw = s_ys + gw * kRows * TT;
+        float* ysw = s_ys + warp * kRows * TT;                  // and the shared expert's
         for (int tile = 0; tile < ytiles; ++tile) {
-            for (int i = lane; i < kRows * TT; i += 32) yw[i] = 0.0f;
-            for (int li = 0; li < nd; ++li) {
-                const Unit u = down_unit(tile, li, nact);
-                const bool routed = li < nact;
+            for (int i = lane; i < kRows * TT; i += 32) yw[i] = ysw[i] = 0.0f;
+            __syncwarp();
+            for_down(nact, tile, [&](const Unit& u, int c0, int c1) {
+                const bool routed = u.e < a.E;
                 const WMat& m = routed ? a.W2 : a.S2;
-                if ((tile * nd + li) % kGroups != grp) continue;
                 const uint32_t mask = s_mask[u.e];
                 const int ncol = __popc(mask), ntn = (ncol + 7) / 8;
                 float acc[NT][4];
@@ -733,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                     const int t = col_token(mask, ncol, n * 8 + g);
                     hp[n] = routed ? a.h + ((size_t)t * a.k + s_slot[t * 256 + u.e]) * a.I : a.hs + (size_t)t * a.Is;
                 }
-                run_unit(m, u, false, false, hp, xp, ntn, acc);
+                run_unit(m, u, c0, c1, false, false, hp, xp, ntn, acc);
                 const float gl = FMT == kNvfp4 ? __ldg(m.glob + (routed ? u.e : 0)) : 1.0f;
                 __syncwarp();
 #pragma unroll
@@ -748,27 +739,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                                 yw[g * TT + t] += w * acc[n][i];
                                 yw[(g + 8) * TT + t] += w * acc[n][2 + i];
                             } else {
-                                ysw[g * TT + t] = gl * acc[n][i];
-                                ysw[(g + 8) * TT + t] = gl * acc[n][2 + i];
+                                ysw[g * TT + t] += gl * acc[n][i];
+                                ysw[(g + 8) * TT + t] += gl * acc[n][2 + i];
                             }
                         }
                     }
                 __syncwarp();
-            }
+                return true;
+            });
             named_bar(5, kCThreads);
-            const Unit u = down_unit(tile, nact, nact);
+            const int r0 = yr0 + part(yr1 - yr0, tile, ytiles), nr = yr0 + part(yr1 - yr0, tile + 1, ytiles) - r0;
             for (int i = tid; i < kRows * TT; i += kCThreads) {
                 const int r = i % kRows, t = i / kRows;
-                if (r >= u.n || t >= a.T || dead) continue;
+                if (r >= nr || t >= a.T || dead) continue;
                 float v = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kCw; ++w) v += s_red[(w * kRows + r) * TT + t];
                 v *= a.out_scale;               // once, on the finished sum
                 if (a.Is > 0) {
 #pragma unroll
-                    for (int w = 0; w < kGw; ++w) v += s_ys[(w * kRows + r) * TT + t];
+                    for (int w = 0; w < kCw; ++w) v += s_ys[(w * kRows + r) * TT + t];
                 }
-                const size_t o = (size_t)t * a.H + u.f0 + r;
+                const size_t o = (size_t)t * a.H + r0 + r;
                 if (a.residual) v += bf16f(a.residual[o]);
                 a.y[o] = f2bf16(v);
             }
