@@ -314,8 +314,9 @@ MOE_API moe_status moe_shared_expert_ex(const void* x, const moe_experts_w* Ws, 
  * its rounding; activations are rounded once to bf16; sums are fp32 and in a
  * fixed order for a given set of picks (no atomics), y is rounded once.
  * Workspace: moe_decode_workspace_bytes(d, Is); its first 256 bytes must be
- * zero before the first call, and every call leaves them zero.  Calls that
- * share a workspace must not overlap on the GPU.  The launch is cooperative
+ * zero before the first call and are the library's from then on (a barrier
+ * count that carries over from call to call).  Calls that share a workspace
+ * must run on one device and not overlap on the GPU.  The launch is cooperative
  * (one CTA per SM, all resident); waits between CTAs are bounded and report
  * device error 2. */
 #define MOE_DECODE_MAX_T 16

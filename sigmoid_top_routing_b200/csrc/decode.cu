@@ -51,6 +51,7 @@ constexpr int kThreads = kCThreads + kGroups * 32;   // + a producer warp per gr
 constexpr int kMaxE = 257;                      // 256 experts and the shared one
 constexpr int kMaxK = 32;
 constexpr int kMaxStages = 16;
+constexpr int kMaxParts = 8;                    // parts of a router row
 
 struct WMat {                                   // one weight tensor of the experts
     const unsigned char* w;
@@ -73,8 +74,9 @@ struct DecodeArgs {
     int32_t* idx;
     float* w;
     uint16_t* y;
-    uint32_t* sync;                             // [0] barrier arrivals, [1] exits; zero between calls
-    double* lg;                                 // (T, E)
+    unsigned long long* sync;                   // barrier arrivals: a multiple of the grid size between calls
+    double* lg;                                 // (parts, T, E): logits, each part over H / parts of the row
+    int parts;
     uint16_t* h;                                // (T k, I)
     uint16_t* hs;                               // (T, Is)
     int stages;                                 // ring slots per group
@@ -98,6 +100,7 @@ struct Layout {                                 // shared memory (byte offsets)
     static constexpr int kRedBytes = kGroups * 2 * kRedBuf;
     static constexpr int kYs = kRed + kRedBytes / 2;                  // the shared expert's y sums per warp
     static constexpr int kX = (kRed + kRedBytes + 127) & ~127;
+    static_assert(kTok * 256 * 4 <= kRedBytes, "the score keys fit them too");
     static_assert(2 * kCw * kRows * kTok * 4 <= kRedBytes, "both y sums fit the group-sum buffers");
 };
 
@@ -108,79 +111,133 @@ MOE_DEV uint64_t key64(double c) {              // order of c; NaN lowest (1), -
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
-// Picks of one token by one warp; lane holds experts lane + 32 i.
-MOE_DEV void select_token(const DecodeArgs& a, int t, int* pick, float* wt, unsigned char* slot, uint32_t* mask,
-                          bool write) {
+MOE_DEV uint32_t key32(float c) {               // the same order for fp32
+    if (c != c) return 1u;
+    if (c == 0.0f) c = 0.0f;
+    const uint32_t u = __float_as_uint(c);
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+MOE_DEV float unkey32(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k); }
+
+MOE_DEV double sigmoid64(double L) { return 1.0 / (1.0 + exp(-L)); }
+
+// The logit of (token t, expert e): given, or the parts' sum in order.
+MOE_DEV double logit_of(const DecodeArgs& a, int t, int e) {
+    if (a.logits) return (double)__ldg(a.logits + (size_t)t * a.E + e);
+    double v[kMaxParts], sum = 0.0;
+#pragma unroll
+    for (int p = 0; p < kMaxParts; ++p) v[p] = p < a.parts ? __ldcg(a.lg + ((size_t)p * a.T + t) * a.E + e) : 0.0;
+#pragma unroll
+    for (int p = 0; p < kMaxParts; ++p) sum += v[p];
+    return sum;
+}
+// Softmax statistics of a token's logits, by one warp: max and sum of exp
+// (NaN when a logit is NaN, which makes every score of the row NaN).
+MOE_DEV void softmax_stats64(const DecodeArgs& a, int t, double& m, double& z) {
     const int lane = threadIdx.x & 31;
-    double s[8];
-    uint64_t key[8];
-    const int ne = (a.E + 31) / 32;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int e = lane + 32 * i;
-        s[i] = 0.0;
-        if (i < ne && e < a.E)
-            s[i] = a.logits ? (double)__ldg(a.logits + (size_t)t * a.E + e) : __ldcg(a.lg + (size_t)t * a.E + e);
-    }
-    if (a.softmax) {                            // a NaN logit makes the row's scores NaN (through the sum)
-        double m = -INFINITY, z = 0.0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (lane + 32 * i < a.E) m = fmax(m, s[i]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (lane + 32 * i < a.E) {
-                s[i] = exp(s[i] - m);
-                z += s[i];
-            }
-#pragma unroll
+    m = -INFINITY;
+    z = 0.0;
+    for (int e = lane; e < a.E; e += 32) m = fmax(m, logit_of(a, t, e));
+    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int e = lane; e < a.E; e += 32) z += exp(logit_of(a, t, e) - m);
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+}
+MOE_DEV double score64(const DecodeArgs& a, double L, double m, double z) {
+    return a.softmax ? (z == z ? exp(L - m) / z : z) : sigmoid64(L);
+}
+
+// Picks of one token by one warp.  s_key[e] holds fp32 score keys (sigmoid) or
+// logits (softmax); lane sees experts lane + 32 i.  The fp32 scores are within
+// 2e-6 (1 + |c|) of the 64-bit ones, so where the first k + 1 of them are
+// further apart than twice that, their order is the 64-bit order; else the
+// token is ranked again from 64-bit scores.  This code runs once per launch, so it is kept short: straight-line code would cost more in
+// instruction fetches than it saves.
+MOE_DEV void select_token(const DecodeArgs& a, int t, uint32_t* s_key, int* pick, unsigned char* slot,
+                          uint32_t* mask) {
+    const int lane = threadIdx.x & 31;
+    if (a.softmax) {
+        float m = -INFINITY, z = 0.0f;
+        for (int e = lane; e < a.E; e += 32) m = fmaxf(m, __uint_as_float(s_key[e]));
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int e = lane; e < a.E; e += 32) z += expf(__uint_as_float(s_key[e]) - m);
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = z == z ? s[i] / z : z;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < ne) s[i] = 1.0 / (1.0 + exp(-s[i]));
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int e = lane + 32 * i;
-        key[i] = e < a.E ? key64(s[i] + (a.ebias ? (double)__ldg(a.ebias + e) : 0.0)) : 0ull;
+        for (int e = lane; e < a.E; e += 32) {
+            const float s = z == z ? expf(__uint_as_float(s_key[e]) - m) / z : z;
+            s_key[e] = key32(s + (a.ebias ? __ldg(a.ebias + e) : 0.0f));
+        }
+        __syncwarp();
     }
     int my_e = 0;
-    double my_s = 0.0, sum = 0.0;
-    for (int j = 0; j < a.k; ++j) {
-        uint64_t best = key[0];
-        int bi = 0;
-        double bs = s[0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i)
-            if (key[i] > best) { best = key[i]; bi = i; bs = s[i]; }
-        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
-        const bool ch = (uint32_t)(best >> 32) == hi;
-        const uint32_t lo = __reduce_max_sync(0xffffffffu, ch ? (uint32_t)best : 0u);
-        const bool win = ch && (uint32_t)best == lo;
-        const uint32_t e = __reduce_min_sync(0xffffffffu, win ? (uint32_t)(lane + 32 * bi) : 0xffffu);
-        const double sj = __shfl_sync(0xffffffffu, bs, e & 31);
-        if (lane == (int)(e & 31)) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i == (int)(e >> 5)) key[i] = 0ull;    // picked: below every NaN
+    bool close = false;
+    uint32_t last = 0;
+    const int rounds = min(a.k + 1, a.E);
+    for (int j = 0; j < rounds; ++j) {
+        uint32_t best = 0;
+        int be = 0xffff;
+        for (int e = lane; e < a.E; e += 32) {
+            const uint32_t c = s_key[e];
+            if (c > best) { best = c; be = e; }
         }
-        if (lane == j) { my_e = (int)e; my_s = sj; }
-        sum += sj;                              // rank order
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)be : 0xffffu);
+        if (lane == (e & 31)) s_key[e] = 0u;    // picked: below every NaN
+        if (lane == j) my_e = e;
+        if (j > 0 && last > 1u && top > 1u) {   // both numbers
+            const float c = unkey32(last);
+            close |= !(c - unkey32(top) > 4e-6f * (1.0f + fabsf(c)));
+        }
+        last = top;
+    }
+    if (close) {                                // warp-uniform
+        double m = 0.0, z = 1.0;
+        if (a.softmax) softmax_stats64(a, t, m, z);
+        uint64_t key[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = lane + 32 * i;
+            key[i] = e < a.E ? key64(score64(a, logit_of(a, t, e), m, z) + (a.ebias ? (double)__ldg(a.ebias + e) : 0.0))
+                             : 0ull;
+        }
+        for (int j = 0; j < a.k; ++j) {
+            uint64_t best = key[0];
+            int bi = 0;
+#pragma unroll
+            for (int i = 1; i < 8; ++i)
+                if (key[i] > best) { best = key[i]; bi = i; }
+            const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
+            const bool ch = (uint32_t)(best >> 32) == hi;
+            const uint32_t lo = __reduce_max_sync(0xffffffffu, ch ? (uint32_t)best : 0u);
+            const bool win = ch && (uint32_t)best == lo;
+            const int e = (int)__reduce_min_sync(0xffffffffu, win ? (uint32_t)(lane + 32 * bi) : 0xffffu);
+            if (lane == (e & 31)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i == (e >> 5)) key[i] = 0ull;
+            }
+            if (lane == j) my_e = e;
+        }
     }
     if (lane < a.k) {
-        const double w = a.no_norm ? my_s * a.scale : my_s / (sum + (double)a.eps) * a.scale;
         pick[lane] = my_e;
-        wt[lane] = (float)w;
         slot[my_e] = (unsigned char)lane;
         atomicOr(mask + my_e, 1u << t);
+    }
+}
+
+// Routing weights of one token's picks by one warp, 64-bit, rounded once.
+MOE_DEV void weigh_token(const DecodeArgs& a, int t, const int* pick, float* wt, bool write) {
+    const int lane = threadIdx.x & 31;
+    double m = 0.0, z = 1.0, s = 0.0, sum = 0.0;
+    if (a.softmax) softmax_stats64(a, t, m, z);
+    const int e = lane < a.k ? pick[lane] : 0;
+    if (lane < a.k) s = score64(a, logit_of(a, t, e), m, z);
+    for (int j = 0; j < a.k; ++j) sum += __shfl_sync(0xffffffffu, s, j);   // rank order
+    if (lane < a.k) {
+        const float w = (float)(a.no_norm ? s * a.scale : s / (sum + (double)a.eps) * a.scale);
+        wt[lane] = w;
         if (write) {
-            a.idx[(size_t)t * a.k + lane] = my_e;
-            a.w[(size_t)t * a.k + lane] = (float)w;
+            a.idx[(size_t)t * a.k + lane] = e;
+            a.w[(size_t)t * a.k + lane] = w;
         }
     }
 }
@@ -476,59 +533,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         const int gw = warp % kGw, gt = tid % (kGw * 32);
         const int g = lane >> 2, t4 = lane & 3;
         bool dead = false;
-        uint32_t target = 0;
-        auto arrive = [&]() {                   // one thread, after a barrier of all consumers
+        // Grid barrier: arrivals only ever add up, gridDim.x per barrier, so what
+        // is there when a CTA looks, rounded down to a multiple of that, is where
+        // the count stood before its next own arrival.
+        unsigned long long target = 0;
+        if (tid == 0) {
+            asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(target) : "l"(a.sync) : "memory");
+            target -= target % (uint32_t)G;
+        }
+        auto arrive = [&]() {                   // thread 0, after a barrier of all consumers
+            target += (uint32_t)G;
             __threadfence();
-            atomicAdd(a.sync, 1u);
+            asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(a.sync), "l"(1ull) : "memory");
         };
-        auto grid_wait = [&]() {                // one thread
+        auto grid_wait = [&]() {                // thread 0
             bool ok = false;
             for (uint32_t i = 0; i < a.wait_limit && !ok; ++i) {
-                uint32_t v;
-                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.sync) : "memory");
+                unsigned long long v;
+                asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(a.sync) : "memory");
                 ok = v >= target;
             }
             if (!ok) {
                 report_error(a.err, kErrWaitExpired);
                 *s_abort = 1;
             }
-            __threadfence();
         };
-        // ---- router: CTA e computes expert e's logits for all tokens
+        // ---- router: work item (expert, part of H); a warp takes one token's
+        // row, or a share of it when there are fewer tokens than warps
         if (!a.logits) {
-            double* s_d = reinterpret_cast<double*>(s_red);      // [kCw][TT]
-            for (int e = cta; e < a.E; e += G) {
-                double acc[TT];
-#pragma unroll
-                for (int t = 0; t < TT; ++t) acc[t] = 0.0;
-                for (int k = tid * 4; k < a.H; k += kCThreads * 4) {
-                    const float4 w = __ldg(reinterpret_cast<const float4*>(a.w_router + (size_t)e * a.H + k));
-#pragma unroll
-                    for (int t = 0; t < TT; ++t)
-                        if (t < a.T) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(a.x + (size_t)t * a.H + k);
-                            acc[t] = fma((double)w.x, (double)bf16lo(v.x), acc[t]);
-                            acc[t] = fma((double)w.y, (double)bf16hi(v.x), acc[t]);
-                            acc[t] = fma((double)w.z, (double)bf16lo(v.y), acc[t]);
-                            acc[t] = fma((double)w.w, (double)bf16hi(v.y), acc[t]);
-                        }
-                }
-#pragma unroll
-                for (int t = 0; t < TT; ++t)
-                    if (t < a.T) {
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-                        if (lane == 0) s_d[warp * TT + t] = acc[t];
+            double* s_d = reinterpret_cast<double*>(s_red);      // [kCw]
+            const int wpt = a.T > 8 ? 1 : a.T > 4 ? 2 : a.T > 2 ? 4 : a.T > 1 ? 8 : 16;   // warps per token
+            const int t = warp / wpt, ws = warp - t * wpt;
+            const int nq = a.H / 4;                              // groups of 4 k
+            for (int it = cta; it < a.E * a.parts; it += G) {
+                const int e = it / a.parts, p = it - e * a.parts;
+                const int q1 = part(nq, p + 1, a.parts);
+                double acc = 0.0;
+                if (t < a.T)
+#pragma unroll 4
+                    for (int q = part(nq, p, a.parts) + ws * 32 + lane; q < q1; q += wpt * 32) {
+                        const float4 w = __ldg(reinterpret_cast<const float4*>(a.w_router + (size_t)e * a.H) + q);
+                        const uint2 v = *(reinterpret_cast<const uint2*>(a.x + (size_t)t * a.H) + q);
+                        acc = fma((double)w.x, (double)bf16lo(v.x), acc);
+                        acc = fma((double)w.y, (double)bf16hi(v.x), acc);
+                        acc = fma((double)w.z, (double)bf16lo(v.y), acc);
+                        acc = fma((double)w.w, (double)bf16hi(v.y), acc);
                     }
+                for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+                if (lane == 0) s_d[warp] = acc;
                 named_bar(5, kCThreads);
                 if (tid < a.T) {
                     double v = 0.0;
-                    for (int w = 0; w < kCw; ++w) v += s_d[w * TT + tid];
-                    __stcg(a.lg + (size_t)tid * a.E + e, v);
+                    for (int w = 0; w < wpt; ++w) v += s_d[tid * wpt + w];
+                    __stcg(a.lg + ((size_t)p * a.T + tid) * a.E + e, v);
                 }
                 named_bar(5, kCThreads);
             }
-            target += G;
             if (tid == 0) arrive();
         }
         // ---- token rows into shared memory (while the other CTAs' logits arrive)
@@ -543,8 +603,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         if (!a.logits && tid == 0) grid_wait();
         named_bar(5, kCThreads);
         // ---- selection: every CTA picks for all tokens, a warp per token
+        uint32_t* s_key = reinterpret_cast<uint32_t*>(s_red);          // [T][E]
+        for (int i = tid; i < a.T * a.E; i += kCThreads) {
+            const int t = i / a.E, e = i - t * a.E;
+            const float L = (float)logit_of(a, t, e);
+            s_key[i] = a.softmax ? __float_as_uint(L)
+                                 : key32(1.0f / (1.0f + expf(-L)) + (a.ebias ? __ldg(a.ebias + e) : 0.0f));
+        }
+        named_bar(5, kCThreads);
         if (warp < a.T)
-            select_token(a, warp, s_pick + warp * kMaxK, s_wt + warp * kMaxK, s_slot + warp * 256, s_mask, cta == 0);
+            select_token(a, warp, s_key + warp * a.E, s_pick + warp * kMaxK, s_slot + warp * 256, s_mask);
         named_bar(5, kCThreads);
         if (warp == 0) {
             int n = 0;
@@ -695,11 +763,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         });
         // ---- every h is written
         named_bar(5, kCThreads);
-        target += G;
-        if (tid == 0) {
-            arrive();
-            grid_wait();
-        }
+        if (tid == 0) arrive();
+        // the weights of the picks are first needed below: they fill the wait
+        if (warp < a.T) weigh_token(a, warp, s_pick + warp * kMaxK, s_wt + warp * kMaxK, cta == 0);
+        if (tid == 0) grid_wait();
         named_bar(5, kCThreads);
         if (*s_abort) dead = true;
 
@@ -767,15 +834,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
             named_bar(5, kCThreads);
         }
     }
-    __syncthreads();
-    // the last CTA out leaves the counters at zero for the next call
-    if (tid == 0) {
-        __threadfence();
-        if (atomicAdd(a.sync + 1, 1u) == (uint32_t)G - 1) {
-            a.sync[0] = 0;
-            a.sync[1] = 0;
-        }
-    }
 }
 
 template <int FMT, int NT, bool DUAL>
@@ -788,6 +846,8 @@ cudaError_t run(DecodeArgs& a, cudaStream_t s) {
     const size_t room = fixed < (size_t)di.max_smem_optin ? di.max_smem_optin - fixed : 0;
     a.sd = F::dims(FMT == kBf16 ? 512 : 2048);
     if (room < (size_t)2 * kGroups * a.sd.bytes) a.sd = F::dims(FMT == kBf16 ? 256 : 1024);
+    // parts of the router's rows: work for all CTAs, at most 8 to sum
+    a.parts = std::max(1, std::min(8, di.sm_count / a.E));
     a.stages = (int)std::min<size_t>(kMaxStages, room / a.sd.bytes) / kGroups;
     if (a.stages < 1) return cudaErrorNotSupported;
     const size_t smem = fixed + (size_t)kGroups * a.stages * a.sd.bytes;
@@ -824,7 +884,7 @@ DecodeWs ws_layout(const moe_dims* d, int Is) {
     L.sync = 0;
     size_t off = 256;
     L.lg = off;
-    off = align256(off + (size_t)d->T * d->E * 8);
+    off = align256(off + (size_t)8 * d->T * d->E * 8);
     L.h = off;
     off = align256(off + (size_t)d->T * d->k * d->I * 2);
     L.hs = off;
@@ -925,7 +985,7 @@ moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void* x, cons
     a.idx = topk_idx;
     a.w = topk_w;
     a.y = static_cast<uint16_t*>(y);
-    a.sync = reinterpret_cast<uint32_t*>(b + wl.sync);
+    a.sync = reinterpret_cast<unsigned long long*>(b + wl.sync);
     a.lg = reinterpret_cast<double*>(b + wl.lg);
     a.h = reinterpret_cast<uint16_t*>(b + wl.h);
     a.hs = reinterpret_cast<uint16_t*>(b + wl.hs);

@@ -120,7 +120,8 @@ def run_and_compare(api, wl, residual=True, logits=None):
     assert api.moe_last_launch_count() == 1
     for b in (yb, ib, wb):
         assert (b[0] == -1).all() and (b[-1] == -1).all()
-    assert (layer.ws[:256] == 0).all()
+    G = torch.cuda.get_device_properties(0).multi_processor_count
+    assert int(layer.ws[:8].view(torch.int64)) % G == 0 and (layer.ws[8:256] == 0).all()
     compare(inp, bits(y), ib[1:-1].cpu().numpy(), wb.view(torch.float32)[1:-1].cpu().numpy(), res, logits)
 
 
