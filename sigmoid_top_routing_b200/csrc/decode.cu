@@ -37,6 +37,7 @@
 #include "internal.h"
 #include "launch.h"
 #include "stream.cuh"
+#include "tmap_rows.h"
 
 namespace moe {
 namespace {
@@ -54,6 +55,8 @@ constexpr int kMaxStages = 16;
 constexpr int kMaxParts = 8;                    // parts of a router row
 
 struct WMat {                                   // one weight tensor of the experts
+    CUtensorMap map;                            // (experts * rows) rows of codes
+    bool flat;                                  // rows are not whole 128-byte chunks
     const unsigned char* w;
     const unsigned char* scale;
     const unsigned char* bias;
@@ -80,7 +83,8 @@ struct DecodeArgs {
     uint16_t* h;                                // (T k, I)
     uint16_t* hs;                               // (T, Is)
     int stages;                                 // ring slots per group
-    StageDims sd;
+    StageDims sd, sd2;                          // stages of the up and the down products
+    int stage_bytes;
     uint32_t wait_limit;
     int* err;
 };
@@ -251,140 +255,79 @@ MOE_DEV int nth_bit(uint32_t m, int c) {
 // A unit of work: rows of one expert against all its tokens.
 struct Unit {
     int e;                                      // expert; a.E: the shared one
-    int n;                                      // rows (per half when dual)
+    int n;                                      // features (up) or rows (down): rows of both halves, or of each when dual
     int f0;                                     // first feature (up) or row of y (down)
-    size_t row0, row1;                          // first weight row; of the up half when dual
+    size_t row0, row1;                          // first weight row of either half of 8 rows
 };
 
 // Start of part i of n equal parts of v (v * (i + 1) must fit 32 bits).
 MOE_DEV int part(int v, int i, int n) { return (int)((uint32_t)v * (uint32_t)i / (uint32_t)n); }
 
-MOE_DEV int chunks_of(int K, const StageDims& sd) { return (K + sd.chunk - 1) / sd.chunk; }
+MOE_DEV int stages_of(int K, const StageDims& sd) { return (K + sd.k - 1) / sd.k; }
 
-// Copies k [k0, k0 + kc) of a unit's rows (and their scales) into a stage.
+// Requests stage c of a unit's rows (and their scales).
 template <int FMT>
-MOE_DEV void issue_stage(const StageDims& sd, const WMat& m, const Unit& u, bool dual, int c, uint32_t dst, uint64_t* bar, uint64_t pol) {
+MOE_DEV void issue_weights(const StageDims& sd, const WMat& m, const Unit& u, bool dual, int c, uint32_t dst,
+                           uint64_t* bar, uint64_t pol) {
     using F = Fmt<FMT>;
     const int lane = threadIdx.x & 31;
-    const int k0 = c * sd.chunk, kc = min(sd.chunk, m.K - k0);
-    bool code = false;
-    size_t R = 0;
-    if (lane < kRows) {
-        const int half = dual ? lane >> 3 : 0, loc = dual ? lane & 7 : lane;
-        code = loc < u.n;
-        R = (half ? u.row1 : u.row0) + loc;
-    }
-    const uint32_t rb = (uint32_t)F::row_bytes(kc);
-    uint32_t bytes = code ? rb : 0, sb = 0, sdst = 0;
+    const bool two = dual || u.n > 8;           // else the second half's rows are nobody's
+    uint32_t sb = 0, sdst = 0;
     size_t s0 = 0;
     if (FMT != kBf16) {
         // scale rows start anywhere: copy the 16-byte aligned span around them
         // (the arrays hold a multiple of 128 bytes, so it stays inside)
         const size_t SB = F::scale_bytes(m.K);
         size_t b = 0, e = 0;
-        if (m.K <= sd.chunk) {                  // whole rows: the unit's rows are one span per half
-            if (lane == 16 || (lane == 17 && dual)) {
-                b = (lane == 17 ? u.row1 : u.row0) * SB;
-                e = b + u.n * SB;
-                sdst = sd.codes + (lane - 16) * (sd.area / 2);
+        if (m.K <= kSpanMaxK) {                 // whole rows: one span per half
+            const int n = dual ? u.n : lane == 0 ? min(u.n, 8) : u.n - 8;
+            if (lane < 2 && n > 0) {
+                b = (lane ? u.row1 : u.row0) * SB;
+                e = b + n * SB;
+                sdst = lane * (sd.area / 2);
             }
-        } else if (code) {
-            b = R * SB + F::scale_bytes(k0);
-            e = b + F::scale_bytes(kc);
-            sdst = sd.codes + lane * sd.slot;
+        } else if (lane < kRows) {
+            const int loc = lane & 7, n = dual || lane < 8 ? min(u.n, 8) : u.n - 8;
+            if (loc < n) {
+                const int k0 = c * sd.k;
+                b = ((lane >= 8 ? u.row1 : u.row0) + loc) * SB + F::scale_bytes(k0);
+                e = b + F::scale_bytes(min(sd.k, m.K - k0));
+                sdst = lane * (sd.area / kRows);
+            }
         }
         if (e > b) {
             s0 = b & ~size_t(15);
             sb = (uint32_t)(((e + 15) & ~size_t(15)) - s0);
         }
-        bytes += sb * (FMT == kAffine ? 2 : 1);
     }
-    const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+    const uint32_t total = (two ? 2u : 1u) * sd.half + (FMT == kBf16 ? 0u : __reduce_add_sync(0xffffffffu, sb)) * (FMT == kAffine ? 2 : 1);
     if (lane == 0) mbar_arrive_expect_tx(bar, total);
     __syncwarp();
-    if (code) bulk_load(dst + lane * sd.row_stride, m.w + R * F::row_bytes(m.K) + F::row_bytes(k0), rb, bar, pol);
-    if (FMT != kBf16 && sb) {
-        bulk_load(dst + sdst, m.scale + s0, sb, bar, pol);
-        if (FMT == kAffine) bulk_load(dst + sdst + sd.area, m.bias + s0, sb, bar, pol);
-    }
-}
-
-// Stage address of the scales of weight row R (MMA row r) of this unit.
-template <int FMT>
-MOE_DEV uint32_t scale_addr(const StageDims& sd, const WMat& m, const Unit& u, bool dual, int r, int c, uint32_t st) {
-    using F = Fmt<FMT>;
-    const int half = dual ? r >> 3 : 0, loc = dual ? r & 7 : r;
-    const size_t base = half ? u.row1 : u.row0;
-    const size_t SB = F::scale_bytes(m.K);
-    if (m.K <= sd.chunk) return st + sd.codes + half * (sd.area / 2) + uint32_t((base * SB) & 15) + loc * (uint32_t)SB;
-    return st + sd.codes + r * sd.slot + uint32_t(((base + loc) * SB + F::scale_bytes(c * sd.chunk)) & 15);
-}
-
-// One step of the products: rows g and g + 8 of the stage against the 8 NT
-// columns held in b (per column 16 bytes bf16, 32 bytes 4-bit).
-template <int FMT, int NT>
-MOE_DEV void step(const StageDims& sd, uint32_t st, int s, uint32_t sc0, uint32_t sc1, const uint4 (&b)[NT][FMT == kBf16 ? 1 : 2],
-                  int ntn, float (&acc)[NT][4]) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t r0 = st + g * sd.row_stride, r1 = r0 + 8 * sd.row_stride;
-    if constexpr (FMT == kBf16) {
-        const uint4 p = lds128(r0 + s * 64 + t * 16), q = lds128(r1 + s * 64 + t * 16);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (n < ntn) {
-                mma_bf16(acc[n], p.x, q.x, p.y, q.y, b[n][0].x, b[n][0].y);
-                mma_bf16(acc[n], p.z, q.z, p.w, q.w, b[n][0].z, b[n][0].w);
-            }
-    } else if constexpr (FMT == kAffine) {
-        // sum_k w x = s sum_k (128 + q) x + (b - 128 s) sum_k x over the step,
-        // which is one group of 64; sum_k x by MMAs against ones
-        const uint2 p = lds64(r0 + s * 32 + t * 8), q = lds64(r1 + s * 32 + t * 8);
-        const float s0 = bf16f(lds_u16(sc0 + s * 2)), s1 = bf16f(lds_u16(sc1 + s * 2));
-        const float b0 = bf16f(lds_u16(sc0 + sd.area + s * 2)) - 128.0f * s0;
-        const float b1 = bf16f(lds_u16(sc1 + sd.area + s * 2)) - 128.0f * s1;
-        constexpr uint32_t one = 0x3F803F80u;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (n < ntn) {
-                float c[4] = {}, x[4] = {};
-                const uint4 u = b[n][0], v = b[n][1];
-                mma_bf16(c, nib_pair(p.x, 0), nib_pair(q.x, 0), nib_pair(p.x, 1), nib_pair(q.x, 1), u.x, u.y);
-                mma_bf16(x, one, one, one, one, u.x, u.y);
-                mma_bf16(c, nib_pair(p.x, 2), nib_pair(q.x, 2), nib_pair(p.x, 3), nib_pair(q.x, 3), u.z, u.w);
-                mma_bf16(x, one, one, one, one, u.z, u.w);
-                mma_bf16(c, nib_pair(p.y, 0), nib_pair(q.y, 0), nib_pair(p.y, 1), nib_pair(q.y, 1), v.x, v.y);
-                mma_bf16(x, one, one, one, one, v.x, v.y);
-                mma_bf16(c, nib_pair(p.y, 2), nib_pair(q.y, 2), nib_pair(p.y, 3), nib_pair(q.y, 3), v.z, v.w);
-                mma_bf16(x, one, one, one, one, v.z, v.w);
-                acc[n][0] += s0 * c[0] + b0 * x[0];
-                acc[n][1] += s0 * c[1] + b0 * x[1];
-                acc[n][2] += s1 * c[2] + b1 * x[0];
-                acc[n][3] += s1 * c[3] + b1 * x[1];
-            }
-    } else {
-        // a lane's 16 k are one scale block: e2m1 * e4m3 exactly in bf16
-        const uint2 p = lds64(r0 + s * 32 + t * 8), q = lds64(r1 + s * 32 + t * 8);
-        const uint32_t e0 = lds_u8(sc0 + s * 4 + t), e1 = lds_u8(sc1 + s * 4 + t);
-        const uint32_t s0 = e4m3x2_to_f16x2(e0 | (e0 << 8)), s1 = e4m3x2_to_f16x2(e1 | (e1 << 8));
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t u[4], v[4];
-            e2m1x8_to_f16(half ? p.y : p.x, u);
-            e2m1x8_to_f16(half ? q.y : q.x, v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                u[i] = f16x2_to_bf16x2(hmul2_u32(u[i], s0));
-                v[i] = f16x2_to_bf16x2(hmul2_u32(v[i], s1));
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                if (n < ntn) {
-                    const uint4 x = b[n][half];
-                    mma_bf16(acc[n], u[0], v[0], u[1], v[1], x.x, x.y);
-                    mma_bf16(acc[n], u[2], v[2], u[3], v[3], x.z, x.w);
-                }
+    if (lane < (two ? 2 : 1)) {
+        const int row = (int)(lane ? u.row1 : u.row0);
+        if (!m.flat) {
+            tma_load_3d(dst + lane * sd.half, &m.map, row, c * sd.chunks, bar, pol);
+        } else {
+            for (int i = 0; i < sd.chunks; ++i)
+                tma_load_rows(dst + lane * sd.half + i * 1024, &m.map, (c * sd.chunks + i) * 128, row, bar, pol);
         }
     }
+    if (FMT != kBf16 && sb) {
+        bulk_load(dst + sd.scales + sdst, m.scale + s0, sb, bar, pol);
+        if (FMT == kAffine) bulk_load(dst + sd.scales + sd.area + sdst, m.bias + s0, sb, bar, pol);
+    }
+}
+
+// Stage address of the scales of row `loc` of a half, at the first step of stage c.
+template <int FMT>
+MOE_DEV uint32_t scale_addr(const StageDims& sd, const WMat& m, const Unit& u, int half, int loc, int c, uint32_t st) {
+    using F = Fmt<FMT>;
+    const size_t base = half ? u.row1 : u.row0;
+    const size_t SB = F::scale_bytes(m.K);
+    if (m.K <= kSpanMaxK)
+        return st + sd.scales + half * (sd.area / 2) + uint32_t((base * SB) & 15) + loc * (uint32_t)SB +
+               (uint32_t)F::scale_bytes(c * sd.k);
+    return st + sd.scales + (half * 8 + loc) * (sd.area / kRows) + uint32_t(((base + loc) * SB + F::scale_bytes(c * sd.k)) & 15);
 }
 
 template <int FMT, int NT, bool DUAL>
@@ -393,9 +336,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
     using L = Layout<NT>;
     constexpr int TT = L::kTok;
     constexpr int kFeat = DUAL ? 8 : kRows;     // features of an up tile
-    constexpr int kB = FMT == kBf16 ? 1 : 2;    // 16-byte pieces of a column per step
-    // steps whose token operand a down warp requests before it waits for the weights
-    constexpr int kAhead = FMT == kBf16 ? 4 : (NT == 1 ? 4 : 2);
     extern __shared__ __align__(128) unsigned char sm[];
     uint32_t* s_mask = reinterpret_cast<uint32_t*>(sm + L::kMask);
     int* s_list = reinterpret_cast<int*>(sm + L::kList);
@@ -407,10 +347,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar);
     uint64_t* empty = full + kMaxStages;
     float* s_red = reinterpret_cast<float*>(sm + L::kRed);
-    float* s_ys = reinterpret_cast<float*>(sm + L::kYs);
     const int xstride = a.H * 2 + F::kXPad;
     const uint32_t xs = smem_u32(sm + L::kX);
-    const uint32_t ring = xs + ((a.T * xstride + 127) & ~127);
+    const uint32_t ring = (xs + a.T * xstride + 1023) & ~1023u;     // swizzled boxes start on 1 KB
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = gridDim.x, cta = blockIdx.x;
@@ -418,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
     for (int i = tid; i < kMaxE; i += kThreads) s_mask[i] = 0;
     if (tid == 0) {
         for (int i = 0; i < kGroups * Sg; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], 2);             // weights, token rows
             mbar_init(&empty[i], kGw);
         }
         *s_abort = 0;
@@ -436,94 +375,157 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
     // This CTA's rows of y, in tiles of at most 16; each tile's list of
     // (expert, chunk of k) is dealt out to the groups in equal parts.
     const int yr0 = part(a.H, cta, G), yr1 = part(a.H, cta + 1, G);
-    const int ytiles = (yr1 - yr0 + kRows - 1) / kRows;
-    const int up_chunks = chunks_of(a.H, a.sd), i_chunks = chunks_of(a.I, a.sd), is_chunks = chunks_of(a.Is, a.sd);
-
-    auto for_shared_up = [&](auto&& f) {        // f(unit) for the group's tiles of the shared expert
-        for (int p = sf0; p < sf1; p += kFeat) {
-            const Unit u{a.E, min(kFeat, sf1 - p), p, (size_t)p, (size_t)a.Is + p};
-            if (!f(u)) return;
-        }
+    const int ytiles = max(1, (yr1 - yr0 + kRows - 1) / kRows);
+    // phases: 0 the shared expert's features, 1 the routed experts', 2.. tiles of y
+    auto rows_of_tile = [&](int tile, int& r0, int& n) {
+        r0 = yr0 + part(yr1 - yr0, tile, ytiles);
+        n = yr0 + part(yr1 - yr0, tile + 1, ytiles) - r0;
     };
-    auto for_routed_up = [&](int nact, auto&& f) {
-        int p = part(nact * a.I, wk, nwk);
-        const int end = part(nact * a.I, wk + 1, nwk);
-        int li = p / a.I, off = p - li * a.I;
+    // Calls f(unit, weights, first chunk, end chunk) for the group's units of a
+    // phase, in order; f returns false to stop.  A down unit is a run of chunks
+    // of one expert: a tile's (expert, chunk) list is dealt out to the groups.
+    auto walk = [&](int phase, int nact, auto&& f) {
+        int p, end, li = 0, off = 0, r0 = 0, nr = 0;
+        const int i_chunks = stages_of(a.I, a.sd2), is_chunks = stages_of(a.Is, a.sd2);
+        if (phase == 0) {
+            p = off = part(a.Is, wk, nwk);
+            end = part(a.Is, wk + 1, nwk);
+        } else if (phase == 1) {
+            p = part(nact * a.I, wk, nwk);
+            end = part(nact * a.I, wk + 1, nwk);
+            li = p / a.I;
+            off = p - li * a.I;
+        } else {
+            rows_of_tile(phase - 2, r0, nr);
+            if (nr == 0) return;                // fewer rows than CTAs
+            const int total = nact * i_chunks + is_chunks;
+            p = part(total, grp, kGroups);
+            end = part(total, grp + 1, kGroups);
+            li = min(p / i_chunks, nact);
+            off = p - li * i_chunks;
+        }
         while (p < end) {
-            const int e = s_list[li], n = min(min(kFeat, a.I - off), end - p);
-            const size_t r = (size_t)e * a.W1.rows + off;
-            if (!f(Unit{e, n, off, r, r + a.I})) return;
-            p += n;
-            off += n;
-            if (off == a.I) {
+            const bool routed = phase != 0 && li < nact;
+            Unit u;
+            u.e = routed ? s_list[li] : a.E;
+            int c0 = 0, c1, took;
+            const int width = phase < 2 ? (routed ? a.I : a.Is) : (routed ? i_chunks : is_chunks);
+            if (phase < 2) {
+                took = u.n = min(min(kFeat, width - off), end - p);
+                u.f0 = off;
+                u.row0 = (routed ? (size_t)u.e * a.W1.rows : 0) + off;
+                u.row1 = u.row0 + (DUAL ? width : 8);
+                c1 = stages_of(a.H, a.sd);
+            } else {
+                took = min(width - off, end - p);
+                u.n = nr;
+                u.f0 = r0;
+                u.row0 = (routed ? (size_t)u.e * a.H : 0) + r0;
+                u.row1 = u.row0 + 8;
+                c0 = off;
+                c1 = off + took;
+            }
+            if (!f(u, phase < 2 ? (routed ? a.W1 : a.S1) : (routed ? a.W2 : a.S2), c0, c1)) return;
+            p += took;
+            off += took;
+            if (off == width) {
                 off = 0;
                 ++li;
             }
         }
     };
-    // f(unit, first chunk, end chunk) for the group's runs of chunks of one row tile
-    auto for_down = [&](int nact, int tile, auto&& f) {
-        const int r0 = yr0 + part(yr1 - yr0, tile, ytiles), r1 = yr0 + part(yr1 - yr0, tile + 1, ytiles);
-        const int total = nact * i_chunks + is_chunks;
-        int q = part(total, grp, kGroups);
-        const int end = part(total, grp + 1, kGroups);
-        while (q < end) {
-            const int li = min(q / i_chunks, nact);
-            const bool routed = li < nact;
-            const int c0 = q - li * i_chunks, c1 = min(routed ? i_chunks : is_chunks, c0 + end - q);
-            const int e = routed ? s_list[li] : a.E;
-            const size_t r = (routed ? (size_t)e * a.H : 0) + r0;
-            if (!f(Unit{e, r1 - r0, r0, r, r}, c0, c1)) return;
-            q += c1 - c0;
-        }
+    // Row of the activations of column c of expert e (its tokens: mask).
+    auto h_row = [&](int e, uint32_t mask, int c) -> const uint16_t* {
+        const int t = nth_bit(mask, c);
+        return e < a.E ? a.h + ((size_t)t * a.k + s_slot[t * 256 + e]) * a.I : a.hs + (size_t)t * a.Is;
     };
 
     if (warp >= kCw) {
         // -------------------------------------------------------- producer of one group
-        const uint64_t pol = policy_evict_first();
+        const uint64_t pol = policy_evict_first(), pol_h = policy_evict_last();
         int slot = 0, fills = 0;                // next ring slot; stages issued
         uint32_t ph = 1;                        // parity of the slot's last release (fresh: passes)
         bool ok = true;
-        auto push = [&](const WMat& m, const Unit& u, bool dual, int c) {
+        // a stage's full barrier takes two arrivals: the weights', the token rows'
+        auto weights = [&](const StageDims& sd, const WMat& m, const Unit& u, bool dual, int c) {
             const int s = ring0 + slot;
             const bool got = mbar_wait(&empty[s], ph, s_abort, a.wait_limit);
             if (!__all_sync(0xffffffffu, got)) {
                 ok = false;
                 return;
             }
-            issue_stage<FMT>(a.sd, m, u, dual, c, ring + s * a.sd.bytes, &full[s], pol);
+            issue_weights<FMT>(sd, m, u, dual, c, ring + s * a.stage_bytes, &full[s], pol);
             ++fills;
             if (++slot == Sg) {
                 slot = 0;
                 ph ^= 1;
             }
         };
+        int hslot = 0, hfills = 0;              // the same for the second arrival
+        auto no_tokens = [&]() {                // up: the columns are read from xs
+            if (lane == 0) mbar_arrive(&full[ring0 + hslot]);
+            ++hfills;
+            hslot = hslot + 1 == Sg ? 0 : hslot + 1;
+        };
+        auto tokens = [&](const Unit& u, int K, int c) {   // down: chunk c of the activations of u's tokens
+            const uint32_t mask = s_mask[u.e];
+            const int n = __popc(mask), s = ring0 + hslot;
+            const int k0 = c * a.sd2.k, kc = min(a.sd2.k, K - k0);
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], n * kc * 2);
+            __syncwarp();
+            if (lane < n)
+                bulk_load(ring + s * a.stage_bytes + a.sd2.tokens + lane * (a.sd2.k * 2 + F::kXPad),
+                          h_row(u.e, mask, lane) + k0, kc * 2, &full[s], pol_h);
+            ++hfills;
+            hslot = hslot + 1 == Sg ? 0 : hslot + 1;
+        };
         // the shared expert's first rows need no routing: fill the free slots with them
         int pre = 0;
-        for_shared_up([&](const Unit& u) {
-            for (int c = 0; c < up_chunks && pre < Sg; ++c, ++pre) push(a.S1, u, DUAL, c);
+        walk(0, 0, [&](const Unit& u, const WMat& m, int c0, int c1) {
+            for (int c = c0; c < c1 && pre < Sg; ++c, ++pre) {
+                weights(a.sd, m, u, DUAL, c);
+                no_tokens();
+            }
             return pre < Sg;
         });
         __syncthreads();                        // routing tables ready
-        int q = 0;
-        for_shared_up([&](const Unit& u) {
-            for (int c = 0; c < up_chunks && ok; ++c)
-                if (q++ >= pre) push(a.S1, u, DUAL, c);
-            return ok;
-        });
         const int nact = *s_nact;
-        for_routed_up(nact, [&](const Unit& u) {
-            for (int c = 0; c < up_chunks && ok; ++c) push(a.W1, u, DUAL, c);
-            return ok;
-        });
-        for (int tile = 0; tile < ytiles; ++tile)
-            for_down(nact, tile, [&](const Unit& u, int c0, int c1) {
-                for (int c = c0; c < c1 && ok; ++c) push(u.e < a.E ? a.W2 : a.S2, u, false, c);
+        for (int phase = 0; phase < 2; ++phase) {
+            int q = phase ? pre : 0;
+            walk(phase, nact, [&](const Unit& u, const WMat& m, int c0, int c1) {
+                for (int c = c0; c < c1 && ok; ++c)
+                    if (q++ >= pre) {
+                        weights(a.sd, m, u, DUAL, c);
+                        if (ok) no_tokens();
+                    }
                 return ok;
             });
+        }
+        // Down: the first Sg stages' weights are requested before h is there.
+        int ahead = 0;
+        walk(2, nact, [&](const Unit& u, const WMat& m, int c0, int c1) {
+            for (int c = c0; c < c1 && ahead < Sg && ok; ++c, ++ahead) weights(a.sd2, m, u, false, c);
+            return ahead < Sg && ok;
+        });
+        named_bar(6, kThreads);                 // every h is written
+        fence_proxy_async_all();
+        if (*s_abort) ok = false;
+        for (int tile = 0; tile < ytiles; ++tile) {
+            int q = tile ? ahead : 0;
+            walk(2 + tile, nact, [&](const Unit& u, const WMat& m, int c0, int c1) {
+                for (int c = c0; c < c1 && ok; ++c) {
+                    if (q++ >= ahead) weights(a.sd2, m, u, false, c);
+                    if (ok) tokens(u, m.K, c);
+                }
+                return ok;
+            });
+        }
         if (!ok) {
             if (lane == 0) report_error(a.err, kErrWaitExpired);
             *s_abort = 1;
+            // stages whose token rows were never sent: let their barriers complete
+            for (; hfills < fills; ++hfills, hslot = hslot + 1 == Sg ? 0 : hslot + 1)
+                if (lane == 0) mbar_arrive(&full[ring0 + hslot]);
         }
         // every copy issued lands before the CTA can exit
         for (int i = max(0, fills - Sg); i < fills; ++i)
@@ -532,6 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         // -------------------------------------------------------- consumers
         const int gw = warp % kGw, gt = tid % (kGw * 32);
         const int g = lane >> 2, t4 = lane & 3;
+        const int sg = F::sigma(g);             // the row of a half that MMA row g is
+        const uint32_t x4 = FMT == kBf16 ? (t4 ^ sg) << 4 : (((t4 >> 1) ^ sg) << 4) | ((t4 & 1) << 3);
         bool dead = false;
         // Grid barrier: arrivals only ever add up, gridDim.x per barrier, so what
         // is there when a CTA looks, rounded down to a multiple of that, is where
@@ -595,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         for (int i = tid; i < a.T * (a.H / 8); i += kCThreads) {
             const int t = i / (a.H / 8), c = i - t * (a.H / 8);
             uint4 v = *(reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H) + c);
-            if (FMT == kAffine)                 // pairs (j, j + 4)
+            if (FMT != kBf16)                   // pairs (j, j + 4)
                 v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                                __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
             *reinterpret_cast<uint4*>(sm + L::kX + (size_t)t * xstride + c * 16) = v;
@@ -632,206 +636,150 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         const int nact = *s_nact;
         int slot = 0;                           // this group's next ring slot, and its parity
         uint32_t ph = 0;
-        // Columns: token of this lane's operand column per 8-token block, and
-        // the row of its activations.
-        auto col_token = [&](uint32_t mask, int ncol, int c) { return nth_bit(mask, c < ncol ? c : 0); };
         float* red = s_red + grp * 2 * (L::kRedBuf / 4);
         int rbuf = 0;
+        float* yw = s_red + warp * kRows * TT;                  // this warp's sums [row][token] of a tile of y
+        float* ysw = reinterpret_cast<float*>(sm + L::kYs) + warp * kRows * TT;   // and the shared expert's
 
-        // the products of one unit: acc = rows x columns over this warp's share of k
-        auto run_unit = [&](const WMat& m, const Unit& u, int c0, int c1, bool dual, bool from_x, const uint16_t* (&hp)[NT],
-                            const uint32_t (&xp)[NT], int ntn, float (&acc)[NT][4]) {
-            for (int c = c0; c < c1; ++c) {
-                const int s = ring0 + slot;
-                const uint32_t st = ring + s * a.sd.bytes;
-                const int k0 = c * a.sd.chunk, steps = min(a.sd.chunk, m.K - k0) / F::kStep;
-                bool waited = false;
-                uint32_t sc0 = 0, sc1 = 0;
-                if (FMT != kBf16) {
-                    sc0 = scale_addr<FMT>(a.sd, m, u, dual, g, c, st);
-                    sc1 = scale_addr<FMT>(a.sd, m, u, dual, g + 8, c, st);
-                }
-                for (int s0 = gw; s0 < steps || !waited; s0 += kGw * kAhead) {
-                    uint4 b[kAhead][NT][kB];
-                    if (!from_x) {
-#pragma unroll
-                        for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                if (s0 + i * kGw < steps && n < ntn) {
-                                    const uint16_t* p = hp[n] + k0 + (s0 + i * kGw) * F::kStep + t4 * (F::kStep / 4);
-#pragma unroll
-                                    for (int q = 0; q < kB; ++q) b[i][n][q] = __ldcg(reinterpret_cast<const uint4*>(p) + q);
-                                }
-                    }
-                    if (!waited) {
-                        waited = true;
-                        if (!dead) {
-                            const bool got = mbar_wait(&full[s], ph, s_abort, a.wait_limit);
-                            if (!__all_sync(0xffffffffu, got)) {
-                                dead = true;
-                                if (lane == 0) report_error(a.err, kErrWaitExpired);
-                                *s_abort = 1;
-                            }
-                        }
-                    }
-                    if (dead) break;
-#pragma unroll
-                    for (int i = 0; i < kAhead; ++i) {
-                        const int si = s0 + i * kGw;
-                        if (si >= steps) break;
-                        if (from_x) {
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                if (n < ntn) {
-                                    const uint32_t p = xp[n] + (k0 + si * F::kStep) * 2 + t4 * (F::kStep / 2);
-#pragma unroll
-                                    for (int q = 0; q < kB; ++q) b[i][n][q] = lds128(p + 16 * q);
-                                }
-                        }
-                        step<FMT, NT>(a.sd, st, si, sc0, sc1, b[i], ntn, acc);
-                    }
-                }
+#pragma unroll 1
+        for (int phase = 0; phase < 2 + ytiles; ++phase) {
+            const bool up = phase < 2;
+            const StageDims& sd = up ? a.sd : a.sd2;
+            if (phase == 2) {                   // every h is written
+                fence_proxy_async_all();        // (the down stages read it through the async proxy)
+                named_bar(5, kCThreads);
+                if (tid == 0) arrive();
+                // the weights of the picks are first needed below: they fill the wait
+                if (warp < a.T) weigh_token(a, warp, s_pick + warp * kMaxK, s_wt + warp * kMaxK, cta == 0);
+                if (tid == 0) grid_wait();
+                named_bar(6, kThreads);
+                if (*s_abort) dead = true;
+            }
+            if (!up) {
+                for (int i = lane; i < kRows * TT; i += 32) yw[i] = ysw[i] = 0.0f;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[s]);
-                if (++slot == Sg) {
-                    slot = 0;
-                    ph ^= 1;
-                }
             }
-        };
-
-        // ---- up projections
-        auto up = [&](const WMat& m, const Unit& u, uint16_t* hbase, int I, float limit) {
-            const uint32_t mask = s_mask[u.e];
-            const int ncol = __popc(mask), ntn = (ncol + 7) / 8;
-            float acc[NT][4];
-            uint32_t xp[NT];
-            const uint16_t* hp[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-                xp[n] = xs + col_token(mask, ncol, n * 8 + g) * xstride;
-                hp[n] = nullptr;
-            }
-            run_unit(m, u, 0, up_chunks, DUAL, true, hp, xp, ntn, acc);
-            // the group's four k shares meet in shared memory
-            float* r = red + rbuf * (L::kRedBuf / 4);
-            rbuf ^= 1;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                if (n < ntn) {
-                    float* p = r + (gw * kRows + g) * TT + n * 8 + 2 * t4;
-                    *reinterpret_cast<float2*>(p) = make_float2(acc[n][0], acc[n][1]);
-                    *reinterpret_cast<float2*>(p + 8 * TT) = make_float2(acc[n][2], acc[n][3]);
-                }
-            named_bar(1 + grp, kGw * 32);
-            const float gl = FMT == kNvfp4 ? __ldg(m.glob + (u.e == a.E ? 0 : u.e)) : 1.0f;
-            for (int i = gt; i < kFeat * ncol; i += kGw * 32) {
-                const int f = i % kFeat, c = i / kFeat;
-                if (f >= u.n || dead) continue;
-                float v = 0.0f, w = 0.0f;
-#pragma unroll
-                for (int q = 0; q < kGw; ++q) {
-                    v += r[(q * kRows + f) * TT + c];
-                    if (DUAL) w += r[(q * kRows + 8 + f) * TT + c];
-                }
-                if (FMT == kNvfp4) {
-                    v *= gl;
-                    w *= gl;
-                }
-                if (DUAL) {
-                    clamp_swiglu(v, w, limit);
-                    v = act_swiglu(v, w);
-                } else {
-                    v = act_relu2(v);
-                }
-                const int t = nth_bit(mask, c);
-                const size_t row = u.e == a.E ? t : (size_t)t * a.k + s_slot[t * 256 + u.e];
-                const int pos = u.f0 + f;
-                // the activation is rounded once to bf16, the down products' operand type
-                __stcg(hbase + row * I + (FMT == kAffine ? affine_pos(pos) : pos), f2bf16(v));
-            }
-        };
-        for_shared_up([&](const Unit& u) {
-            up(a.S1, u, a.hs, a.Is, a.limit_s);
-            return true;
-        });
-        for_routed_up(nact, [&](const Unit& u) {
-            up(a.W1, u, a.h, a.I, a.limit);
-            return true;
-        });
-        // ---- every h is written
-        named_bar(5, kCThreads);
-        if (tid == 0) arrive();
-        // the weights of the picks are first needed below: they fill the wait
-        if (warp < a.T) weigh_token(a, warp, s_pick + warp * kMaxK, s_wt + warp * kMaxK, cta == 0);
-        if (tid == 0) grid_wait();
-        named_bar(5, kCThreads);
-        if (*s_abort) dead = true;
-
-        // ---- down projections
-        float* yw = s_red + warp * kRows * TT;                  // this warp's sums [row][token]
-        float* ysw = s_ys + warp * kRows * TT;                  // and the shared expert's
-        for (int tile = 0; tile < ytiles; ++tile) {
-            for (int i = lane; i < kRows * TT; i += 32) yw[i] = ysw[i] = 0.0f;
-            __syncwarp();
-            for_down(nact, tile, [&](const Unit& u, int c0, int c1) {
-                const bool routed = u.e < a.E;
-                const WMat& m = routed ? a.W2 : a.S2;
+            walk(phase, nact, [&](const Unit& u, const WMat& m, int c0, int c1) {
                 const uint32_t mask = s_mask[u.e];
                 const int ncol = __popc(mask), ntn = (ncol + 7) / 8;
                 float acc[NT][4];
-                uint32_t xp[NT];
-                const uint16_t* hp[NT];
+                uint32_t col[NT];               // this lane's column of each block of 8: offset of its first k
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-                    xp[n] = 0;
-                    const int t = col_token(mask, ncol, n * 8 + g);
-                    hp[n] = routed ? a.h + ((size_t)t * a.k + s_slot[t * 256 + u.e]) * a.I : a.hs + (size_t)t * a.Is;
+                    const int c = n * 8 + g < ncol ? n * 8 + g : 0;
+                    col[n] = (up ? xs + nth_bit(mask, c) * xstride : a.sd2.tokens + c * (a.sd2.k * 2 + F::kXPad)) +
+                             t4 * (FMT == kBf16 ? 16 : 32);
                 }
-                run_unit(m, u, c0, c1, false, false, hp, xp, ntn, acc);
-                const float gl = FMT == kNvfp4 ? __ldg(m.glob + (routed ? u.e : 0)) : 1.0f;
-                __syncwarp();
+                for (int c = c0; c < c1; ++c) {
+                    const int s = ring0 + slot, steps = min(sd.k, m.K - c * sd.k) / kStep;
+                    const uint32_t st = ring + s * a.stage_bytes;
+                    const int s0 = steps * gw / kGw, n = steps * (gw + 1) / kGw - s0;
+                    uint32_t xb[NT], sc0 = 0, sc1 = 0;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int c = n * 8 + 2 * t4 + i;
-                        if (c < ncol) {
-                            const int t = nth_bit(mask, c);
-                            if (routed) {
-                                const float w = s_wt[t * kMaxK + s_slot[t * 256 + u.e]] * gl;
-                                yw[g * TT + t] += w * acc[n][i];
-                                yw[(g + 8) * TT + t] += w * acc[n][2 + i];
-                            } else {
-                                ysw[g * TT + t] += gl * acc[n][i];
-                                ysw[(g + 8) * TT + t] += gl * acc[n][2 + i];
-                            }
+                    for (int i = 0; i < NT; ++i) xb[i] = col[i] + (up ? c * sd.k * 2 : st) + s0 * (kStep * 2);
+                    if (FMT != kBf16) {
+                        const uint32_t o = s0 * (FMT == kAffine ? 2 : 4) + (FMT == kNvfp4 ? t4 : 0);
+                        sc0 = scale_addr<FMT>(sd, m, u, 0, sg, c, st) + o;
+                        sc1 = scale_addr<FMT>(sd, m, u, 1, sg, c, st) + o;
+                    }
+                    if (!dead) {
+                        const bool got = mbar_wait(&full[s], ph, s_abort, a.wait_limit);
+                        if (!__all_sync(0xffffffffu, got)) {
+                            dead = true;
+                            if (lane == 0) report_error(a.err, kErrWaitExpired);
+                            *s_abort = 1;
                         }
                     }
-                __syncwarp();
+                    if (!dead) {
+                        run_steps<FMT, NT>(st + sg * 128, sd.half, x4, s0, n, sc0, sc1, sd.area, xb, ntn, acc);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[s]);
+                    if (++slot == Sg) {
+                        slot = 0;
+                        ph ^= 1;
+                    }
+                }
+                // NVFP4: the expert's global scale (the products carry 2^-8)
+                const float gl = FMT == kNvfp4 ? 256.0f * __ldg(m.glob + (u.e == a.E ? 0 : u.e)) : 1.0f;
+                if (up) {
+                    // the group's four k shares meet in shared memory
+                    float* r = red + rbuf * (L::kRedBuf / 4);
+                    rbuf ^= 1;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        if (n < ntn) {
+                            float* p = r + (gw * kRows + sg) * TT + n * 8 + 2 * t4;
+                            *reinterpret_cast<float2*>(p) = make_float2(acc[n][0], acc[n][1]);
+                            *reinterpret_cast<float2*>(p + 8 * TT) = make_float2(acc[n][2], acc[n][3]);
+                        }
+                    named_bar(1 + grp, kGw * 32);
+                    for (int i = gt; i < kFeat * ncol; i += kGw * 32) {
+                        const int f = i % kFeat, c = i / kFeat;
+                        if (f >= u.n || dead) continue;
+                        float v = 0.0f, w = 0.0f;
+#pragma unroll
+                        for (int q = 0; q < kGw; ++q) {
+                            v += r[(q * kRows + f) * TT + c];
+                            if (DUAL) w += r[(q * kRows + 8 + f) * TT + c];
+                        }
+                        if (FMT == kNvfp4) {
+                            v *= gl;
+                            w *= gl;
+                        }
+                        if (DUAL) {
+                            clamp_swiglu(v, w, u.e == a.E ? a.limit_s : a.limit);
+                            v = act_swiglu(v, w);
+                        } else {
+                            v = act_relu2(v);
+                        }
+                        // the activation is rounded once to bf16, the down products' operand type
+                        const int pos = u.f0 + f;
+                        __stcg(const_cast<uint16_t*>(h_row(u.e, mask, c)) + (FMT == kBf16 ? pos : pair_pos(pos)), f2bf16(v));
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int c = n * 8 + 2 * t4 + i;
+                            if (c < ncol) {
+                                const int t = nth_bit(mask, c);
+                                const bool routed = u.e < a.E;
+                                const float w = (routed ? s_wt[t * kMaxK + s_slot[t * 256 + u.e]] : 1.0f) * gl;
+                                float* y = routed ? yw : ysw;
+                                y[sg * TT + t] += w * acc[n][i];
+                                y[(sg + 8) * TT + t] += w * acc[n][2 + i];
+                            }
+                        }
+                    __syncwarp();
+                }
                 return true;
             });
-            named_bar(5, kCThreads);
-            const int r0 = yr0 + part(yr1 - yr0, tile, ytiles), nr = yr0 + part(yr1 - yr0, tile + 1, ytiles) - r0;
-            for (int i = tid; i < kRows * TT; i += kCThreads) {
-                const int r = i % kRows, t = i / kRows;
-                if (r >= nr || t >= a.T || dead) continue;
-                float v = 0.0f;
+            if (!up) {
+                int r0, nr;
+                rows_of_tile(phase - 2, r0, nr);
+                named_bar(5, kCThreads);
+                for (int i = tid; i < kRows * TT; i += kCThreads) {
+                    const int r = i % kRows, t = i / kRows;
+                    if (r >= nr || t >= a.T || dead) continue;
+                    const size_t o = (size_t)t * a.H + r0 + r;
+                    const float res = a.residual ? bf16f(a.residual[o]) : 0.0f;
+                    float v = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kCw; ++w) v += s_red[(w * kRows + r) * TT + t];
-                v *= a.out_scale;               // once, on the finished sum
-                if (a.Is > 0) {
-#pragma unroll
-                    for (int w = 0; w < kCw; ++w) v += s_ys[(w * kRows + r) * TT + t];
+                    for (int w = 0; w < kCw; ++w) v += s_red[(w * kRows + r) * TT + t];
+                    v *= a.out_scale;           // once, on the finished sum
+                    if (a.Is > 0) {
+                        float sh = 0.0f;
+                        for (int w = 0; w < kCw; ++w) sh += s_red[L::kRedBytes / 8 + (w * kRows + r) * TT + t];
+                        v += sh;
+                    }
+                    if (a.residual) v += res;
+                    a.y[o] = f2bf16(v);
                 }
-                const size_t o = (size_t)t * a.H + r0 + r;
-                if (a.residual) v += bf16f(a.residual[o]);
-                a.y[o] = f2bf16(v);
+                named_bar(5, kCThreads);
             }
-            named_bar(5, kCThreads);
         }
     }
 }
@@ -840,20 +788,40 @@ template <int FMT, int NT, bool DUAL>
 cudaError_t run(DecodeArgs& a, cudaStream_t s) {
     const DeviceInfo& di = device_info();
     using F = Fmt<FMT>;
-    const size_t fixed = Layout<NT>::kX + (((size_t)a.T * (a.H * 2 + F::kXPad) + 127) & ~size_t(127));
-    // 1 KB of each row a stage, or 512 bytes where the token rows leave room
-    // for less than two slots per group
-    const size_t room = fixed < (size_t)di.max_smem_optin ? di.max_smem_optin - fixed : 0;
-    a.sd = F::dims(FMT == kBf16 ? 512 : 2048);
-    if (room < (size_t)2 * kGroups * a.sd.bytes) a.sd = F::dims(FMT == kBf16 ? 256 : 1024);
+    // + 1 KB: the ring starts on a multiple of that
+    const size_t fixed = Layout<NT>::kX + (size_t)a.T * (a.H * 2 + F::kXPad) + 1024;
+    const int room = fixed < (size_t)di.max_smem_optin ? (int)(di.max_smem_optin - fixed) : 0;
+    // Two slots per group of 16 KB of weights each where they fit, smaller ones
+    // (at last a single one) where the token rows leave less room.  Down stages
+    // hold the columns' activations too: as many chunks as fit behind them.
+    auto up = [&](int c) { return F::dims(c, a.H, 0, 0); };
+    auto down = [&](int c) { return F::dims(c, a.I, a.Is, a.T); };
+    int slots = 3, c1, c2;
+    do {
+        const int most = room / (--slots * kGroups);
+        for (c1 = 8; c1 > 1 && up(c1).bytes > most;) --c1;
+        for (c2 = 8; c2 > 1 && down(c2).bytes > most;) --c2;
+    } while (slots > 1 && (c1 == 1 || c2 == 1));
+    a.sd = up(c1);
+    a.sd2 = down(c2);
+    a.stage_bytes = std::max(a.sd.bytes, a.sd2.bytes);
+    a.stages = std::min(kMaxStages, room / a.stage_bytes) / kGroups;
+    if (a.stages < 1) return cudaErrorNotSupported;
+    const size_t smem = fixed + (size_t)kGroups * a.stages * a.stage_bytes;
+    const int n1 = a.E * a.W1.rows, n2 = a.E * a.W2.rows;
+    auto map = [&](WMat& m, int rows, int chunks) {
+        const uint64_t bytes = FMT == kBf16 ? (uint64_t)m.K * 2 : (uint64_t)m.K / 2;
+        return make_tmap_rows(&m.map, m.w, bytes, bytes, rows, 8, chunks, &m.flat);
+    };
+    cudaError_t e = map(a.W1, n1, c1);
+    if (e == cudaSuccess) e = map(a.W2, n2, c2);
+    if (e == cudaSuccess && a.Is > 0) e = map(a.S1, a.S1.rows, c1);
+    if (e == cudaSuccess && a.Is > 0) e = map(a.S2, a.S2.rows, c2);
+    if (e != cudaSuccess) return e;
     // parts of the router's rows: work for all CTAs, at most 8 to sum
     a.parts = std::max(1, std::min(8, di.sm_count / a.E));
-    a.stages = (int)std::min<size_t>(kMaxStages, room / a.sd.bytes) / kGroups;
-    if (a.stages < 1) return cudaErrorNotSupported;
-    const size_t smem = fixed + (size_t)kGroups * a.stages * a.sd.bytes;
     auto kern = k_decode<FMT, NT, DUAL>;
-    cudaError_t e = ensure_smem(kern, smem);
-    if (e != cudaSuccess) return e;
+    if ((e = ensure_smem(kern, smem)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(di.sm_count);
     cfg.blockDim = dim3(kThreads);
@@ -910,8 +878,14 @@ moe_status check_sizes(const moe_dims* d, int Is) {
 }
 
 WMat mat(const void* w, const void* scale, const void* bias, const float* glob, int rows, int K) {
-    return WMat{static_cast<const unsigned char*>(w), static_cast<const unsigned char*>(scale),
-                static_cast<const unsigned char*>(bias), glob, rows, K};
+    WMat m{};
+    m.w = static_cast<const unsigned char*>(w);
+    m.scale = static_cast<const unsigned char*>(scale);
+    m.bias = static_cast<const unsigned char*>(bias);
+    m.glob = glob;
+    m.rows = rows;
+    m.K = K;
+    return m;
 }
 
 bool misaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
