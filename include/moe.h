@@ -77,7 +77,7 @@ typedef enum {
     MOE_ERR_DEVICE = 7       /* moe_device_error found a device-side error code */
 } moe_status;
 
-typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_RELU2 = 1 } moe_act;
+typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_RELU2 = 1, MOE_ACT_NONE = 2 /* moe_linear only */ } moe_act;
 typedef enum { MOE_W_BF16 = 0, MOE_W_AFFINE4_G64 = 1, MOE_W_NVFP4 = 2 } moe_wfmt;
 
 /* Which expert kernels run (per call through moe_exec_cfg, or the process-wide
@@ -333,6 +333,36 @@ MOE_API size_t moe_decode_workspace_bytes(const moe_dims* d, int32_t Is);
 MOE_API moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void* x, const float* logits,
                               const void* residual, int32_t* topk_idx, float* topk_w, void* y, void* ws,
                               size_t ws_bytes, moe_stream_t stream);
+
+/* A linear layer with bias, activation and residual in the product's epilogue,
+ *   y[m, n] = act(sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n],
+ * for the dense layers beside the MoE block (and a shared expert built from
+ * two of them), from one token to many thousands.
+ *   x         bf16 (M, K), row stride ldx
+ *   w         bf16 (N, K), row stride ldw; act SWIGLU: (2N, K), rows [0, N) gate,
+ *             [N, 2N) up, and act = silu(g) u with swiglu_limit's clamp of the
+ *             inputs (0 = off), as for the experts
+ *   bias      fp32 (N), or (2N) for SWIGLU, or NULL; added before the activation
+ *   residual  bf16 or (res_f32 = 1) fp32 (M, N), row stride ldr, or NULL; added
+ *             after the activation
+ *   y         bf16 or (y_f32 = 1) fp32 (M, N), row stride ldy.  y may be residual
+ *             (same pointer, type and stride); it must not overlap x or w.
+ * Row strides are in elements, 0 = dense.  x and w are 16-byte aligned with
+ * strides that are multiples of 8 elements (MOE_ERR_ALIGN); residual and y only
+ * to their element, with any stride >= N.  0 <= M, 1 <= N, 1 <= K, each up to 2^24.
+ * Sums are fp32; the result is rounded once, at the store.  No workspace; the
+ * same sizes give the same bits every time. */
+typedef struct {
+    int32_t M, N, K;
+    int64_t ldx, ldw, ldr, ldy;
+} moe_linear_dims;
+typedef struct {
+    int32_t act; /* MOE_ACT_NONE, MOE_ACT_RELU2 or MOE_ACT_SWIGLU */
+    int32_t res_f32, y_f32;
+    float swiglu_limit;
+} moe_linear_cfg;
+MOE_API moe_status moe_linear(const void* x, const void* w, const float* bias, const void* residual,
+                              const moe_linear_dims* d, const moe_linear_cfg* cfg, void* y, moe_stream_t stream);
 
 /* moe_forward with HOST buffers for the token rows: x_host (T, H) bf16 is
  * copied to x_dev, the block runs, and y_dev is copied back to y_host (T, H)

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int32, c_size_t, c_void_p
+from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libmoe_b200.so")
 
@@ -17,7 +17,7 @@ MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED, MOE_ERR
     MOE_ERR_CUDA, MOE_ERR_DEVICE = range(8)
 STATUS_NAMES = ["MOE_OK", "MOE_ERR_NULL", "MOE_ERR_SHAPE", "MOE_ERR_ALIGN", "MOE_ERR_UNSUPPORTED",
                 "MOE_ERR_WORKSPACE", "MOE_ERR_CUDA", "MOE_ERR_DEVICE"]
-MOE_ACT_SWIGLU, MOE_ACT_RELU2 = 0, 1
+MOE_ACT_SWIGLU, MOE_ACT_RELU2, MOE_ACT_NONE = 0, 1, 2
 MOE_W_BF16, MOE_W_AFFINE4_G64, MOE_W_NVFP4 = 0, 1, 2
 MOE_DISPATCH_AUTO, MOE_DISPATCH_GEMV, MOE_DISPATCH_GEMM = 0, 1, 2
 MOE_COMBINE_ATOMIC, MOE_COMBINE_ORDERED = 0, 1
@@ -62,6 +62,15 @@ class moe_layer(ctypes.Structure):
                 ("router", moe_router_cfg)]
 
 
+class moe_linear_dims(ctypes.Structure):
+    _fields_ = [("M", c_int32), ("N", c_int32), ("K", c_int32),
+                ("ldx", c_int64), ("ldw", c_int64), ("ldr", c_int64), ("ldy", c_int64)]
+
+
+class moe_linear_cfg(ctypes.Structure):
+    _fields_ = [("act", c_int32), ("res_f32", c_int32), ("y_f32", c_int32), ("swiglu_limit", c_float)]
+
+
 # name -> (restype, argtypes), exactly the declarations of include/moe.h
 PROTOTYPES = {
     "moe_workspace_bytes": (c_size_t, [POINTER(moe_dims), c_int32]),
@@ -90,6 +99,8 @@ PROTOTYPES = {
                                     c_size_t, c_void_p]),
     "moe_shared_expert_ex": (c_int32, [c_void_p, POINTER(moe_experts_w), POINTER(moe_dims),
                                        POINTER(moe_exec_cfg), c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_linear": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, POINTER(moe_linear_dims), POINTER(moe_linear_cfg),
+                             c_void_p, c_void_p]),
     "moe_decode_workspace_bytes": (c_size_t, [POINTER(moe_dims), c_int32]),
     "moe_decode": (c_int32, [POINTER(moe_layer), POINTER(moe_dims), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                              c_void_p, c_void_p, c_size_t, c_void_p]),

@@ -21,6 +21,7 @@ __all__ = [
     "moe_device_error",
     "moe_last_error", "moe_version", "new_plan", "new_workspace", "dims", "moe_profile_hook",
     "moe_last_launch_count", "exec_cfg", "moe_experts_ex", "DecodeLayer", "moe_decode_workspace_bytes",
+    "moe_linear",
 ]
 
 
@@ -232,6 +233,60 @@ def moe_forward_host(x_host: torch.Tensor, x_dev, W: ExpertWeights, w_router, ex
                                   _ptr(topk_idx), _ptr(topk_w), ctypes.byref(cp), _ptr(y_dev),
                                   y_host.data_ptr(), _ptr(ws), ws.numel(), _stream(stream)), "moe_forward_host")
     return y_host
+
+
+_LINEAR_ACT = {"none": abi.MOE_ACT_NONE, "relu2": abi.MOE_ACT_RELU2, "swiglu": abi.MOE_ACT_SWIGLU}
+
+
+def _rows(name: str, t: torch.Tensor, rows: int, cols: int, dtypes, device) -> int:
+    """Row stride of a (rows, cols) matrix with unit column stride, or ValueError."""
+    if t.device != device or t.dtype not in dtypes or t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name}: expected ({rows}, {cols}) of {dtypes[0]} on {device}, got {tuple(t.shape)} of "
+                         f"{t.dtype} on {t.device}")
+    s0, s1 = t.stride()
+    if (s1 != 1 and cols > 1) or (s0 < cols and rows > 1):
+        raise ValueError(f"{name}: expected unit column stride and rows that do not overlap, got strides {t.stride()}")
+    return s0 if rows > 1 else (cols + 7) // 8 * 8   # the stride of a single row means nothing
+
+
+def moe_linear(x, w, bias=None, residual=None, *, act: str = "none", swiglu_limit: float = 0.0, out_dtype=None, y=None,
+               stream=None):
+    """y = act(x w^T + bias) + residual (``act``: "none", "relu2" or "swiglu", the
+    last with w = [gate; up] of 2N rows).  x (M, K) and w are bf16 with row strides
+    that are multiples of 8; bias is fp32; residual and y are bf16 or fp32 with any
+    row stride.  y defaults to a new bf16 (or ``out_dtype``) tensor; it may be the
+    residual itself."""
+    if not x.is_cuda or x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w: expected CUDA matrices")
+    dev, (M, K), rows = x.device, x.shape, w.shape[0]
+    if act not in _LINEAR_ACT:
+        raise ValueError(f"act: expected one of {sorted(_LINEAR_ACT)}, got {act!r}")
+    if act == "swiglu" and rows % 2:
+        raise ValueError("w: swiglu needs an even number of rows (gate, then up)")
+    N = rows // 2 if act == "swiglu" else rows
+    ldx = _rows("x", x, M, K, (torch.bfloat16,), dev)
+    ldw = _rows("w", w, rows, K, (torch.bfloat16,), dev)
+    _want("bias", bias, (rows,), (torch.float32,), dev)
+    out = (torch.bfloat16, torch.float32)
+    ldr = _rows("residual", residual, M, N, out, dev) if residual is not None else N
+    if y is None:
+        y = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
+    elif out_dtype is not None and y.dtype != out_dtype:
+        raise ValueError(f"y is {y.dtype}, out_dtype is {out_dtype}")
+    ldy = _rows("y", y, M, N, out, dev)
+    d = abi.moe_linear_dims(M, N, K, ldx, ldw, ldr, ldy)
+    cfg = abi.moe_linear_cfg(_LINEAR_ACT[act], residual is not None and residual.dtype == torch.float32,
+                             y.dtype == torch.float32, swiglu_limit)
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _linear(x, w, bias, residual, d, cfg, y, stream)
+    return _linear(x, w, bias, residual, d, cfg, y, stream)
+
+
+def _linear(x, w, bias, residual, d, cfg, y, stream):
+    check(load().moe_linear(x.data_ptr(), w.data_ptr(), _ptr(bias), None if residual is None else residual.data_ptr(),
+                            ctypes.byref(d), ctypes.byref(cfg), y.data_ptr(), _stream(stream)), "moe_linear")
+    return y
 
 
 def moe_decode_workspace_bytes(d: abi.moe_dims, Is: int = 0) -> int:

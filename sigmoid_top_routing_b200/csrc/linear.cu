@@ -1,0 +1,644 @@
+// A linear layer with bias, activation and residual in the product's epilogue:
+//
+//   y[m, n] = act(sum_k x[m, k] W[n, k] + bias[n]) + residual[m, n]
+//
+// act none, relu(v)^2, or SwiGLU over W = [gate; up] (2N rows): silu(g) u.
+// bf16 x and W, fp32 sums, one rounding at the store (none for fp32 y).
+//
+// Both kernels put weight rows on the MMA's M (A operand) and tokens on its N,
+// so a few tokens cost a narrow MMA, and a TMEM lane is a feature: its bias is
+// one register and the 32 lanes of a warp store 32 neighbouring features of a
+// token, for any N and any alignment of the rows.  For SwiGLU a 128-row A tile
+// holds 64 features: within each 32-lane quarter of TMEM, lanes 0-15 are gate
+// rows and 16-31 the matching up rows (one TMA box of 16 rows x 2 halves per
+// quarter), so gate and up meet by one warp shuffle.
+//
+//   k_linear_pair   persistent, 256 x BN tiles on SM pairs (cta_group::2), for
+//                   products with enough tiles to fill the SMs.  Each CTA loads
+//                   its 128 weight rows and half of the token rows per k-block
+//                   of 64 into a ring of 6 stages; two TMEM accumulators let the
+//                   epilogue of one tile overlap the next one's MMAs.
+//   k_linear_split  one 128 x BN tile per cluster of ks CTAs that share its K,
+//                   for few tokens or small products: partial sums meet through
+//                   distributed shared memory in rank order, so no workspace, no
+//                   atomics, and the same bits every time.
+//
+// Rows and k past the ends are zero-filled by TMA on both operands.  Every wait
+// is bounded; on expiry the kernel records device error 2, drains and returns.
+#include <cuda.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+#include "launch.h"
+#include "sm100.cuh"
+
+namespace moe {
+namespace {
+
+using namespace sm100;
+
+constexpr int kBK = 64;                          // k per stage: one 128-byte swizzle row
+constexpr int kAStage = 128 * kBK * 2;           // 16 KB of weight rows per CTA
+constexpr int kLinThreads = 192;                 // producer, MMA issuer, 4 epilogue warps
+constexpr int kMaxStage = 8;
+
+struct LinParams {
+    const float* bias;
+    const void* residual;
+    void* y;
+    long long ldr, ldy;                          // row strides in elements
+    int M, N, nkb;                               // tokens, features, k-blocks
+    int n_wt, n_tt, BN;                          // weight tiles, token tiles, tokens of a tile
+    int stages, ks;
+    int res_f32, y_f32;
+    float limit;
+    uint32_t wait_limit;
+    int* err;
+};
+
+// Epilogue of NC columns (tokens t0 .. t0 + NC - 1) of this lane's feature row.
+// f: the lane's feature (SwiGLU: the same for lanes l and l + 16).
+template <int ACT, int NC>
+MOE_DEV void emit(const LinParams& p, const float (&v)[NC], int f, int t0, float b0, float b1) {
+    constexpr int C = ACT == MOE_ACT_SWIGLU ? NC / 2 : NC;       // columns this lane stores
+    const int lane = threadIdx.x & 31;
+    float o[C];
+    int t = t0;
+    if constexpr (ACT == MOE_ACT_SWIGLU) {
+        // low lanes end up with gate and up of the first half of the columns, high lanes of the second
+        const bool lo = lane < 16;
+        if (!lo) t += C;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, lo ? v[C + i] : v[i], 16);
+            float g = (lo ? v[i] : other) + b0, u = (lo ? other : v[C + i]) + b1;
+            clamp_swiglu(g, u, p.limit);
+            o[i] = act_swiglu(g, u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[i] = ACT == MOE_ACT_RELU2 ? act_relu2(v[i] + b0) : v[i] + b0;
+    }
+    if (f >= p.N) return;
+    const int n = min(C, p.M - t);
+    if (p.residual) {
+        if (p.res_f32) {
+            const float* r = static_cast<const float*>(p.residual) + (size_t)t * p.ldr + f;
+            float q[C];
+#pragma unroll
+            for (int i = 0; i < C; ++i) q[i] = i < n ? r[(size_t)i * p.ldr] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < C; ++i) o[i] += q[i];
+        } else {
+            const uint16_t* r = static_cast<const uint16_t*>(p.residual) + (size_t)t * p.ldr + f;
+            uint16_t q[C];
+#pragma unroll
+            for (int i = 0; i < C; ++i) q[i] = i < n ? r[(size_t)i * p.ldr] : uint16_t(0);
+#pragma unroll
+            for (int i = 0; i < C; ++i) o[i] += bf16f(q[i]);
+        }
+    }
+    if (p.y_f32) {
+        float* y = static_cast<float*>(p.y) + (size_t)t * p.ldy + f;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (i < n) y[(size_t)i * p.ldy] = o[i];
+    } else {
+        uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)t * p.ldy + f;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (i < n) y[(size_t)i * p.ldy] = f2bf16(o[i]);
+    }
+}
+
+// Feature of TMEM lane `row` (0..127) of a CTA's tile that starts at feature f0.
+template <int ACT>
+MOE_DEV int feature_of(int f0, int row) {
+    return ACT == MOE_ACT_SWIGLU ? f0 + 16 * (row >> 5) + (row & 15) : f0 + row;
+}
+template <int ACT>
+MOE_DEV void bias_of(const LinParams& p, int f, float& b0, float& b1) {
+    b0 = b1 = 0.0f;
+    if (p.bias && f < p.N) {
+        b0 = __ldg(p.bias + f);
+        if (ACT == MOE_ACT_SWIGLU) b1 = __ldg(p.bias + p.N + f);
+    }
+}
+
+// 3D tiled load (SwiGLU weights: k, row, gate / up half).
+MOE_DEV void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+MOE_DEV void tma_load_3d_pair(void* dst, const CUtensorMap* m, int x, int y, int z, uint32_t cbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(cbar)
+        : "memory");
+}
+
+// Tile t of the persistent order: weight tiles in groups of 8, token tiles
+// within a group, so the tiles running at one time share operands in L2.
+MOE_DEV void tile_of(const LinParams& p, int t, int& wt, int& tt) {
+    const int per = 8 * p.n_tt, g = t / per, r = t - g * per;
+    const int gw = min(8, p.n_wt - g * 8);
+    tt = r / gw;
+    wt = g * 8 + r - tt * gw;
+}
+
+constexpr int kPairStages = 6;
+constexpr size_t kPairSmem = size_t(kPairStages) * 2 * kAStage + 1024 + 256;
+
+template <int ACT>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    k_linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, LinParams p) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* sm =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* sA = sm;
+    unsigned char* sB = sm + kPairStages * kAStage;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sB + kPairStages * kAStage);
+    uint64_t* empty = full + kPairStages;
+    uint64_t* tfull = empty + kPairStages;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    constexpr int kF = ACT == MOE_ACT_SWIGLU ? 64 : 128;         // features of a CTA's 128 rows
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 8);
+        }
+        mbar_init(drain, 1);
+        *s_abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    cluster_sync();                              // both CTAs' barriers exist before either signals the other
+    if (warp == 1) {
+        tmem_alloc_pair(s_tmem, 512);
+        tmem_relinquish_pair();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    pdl_wait();
+    pdl_trigger();
+    const int total = p.n_wt * p.n_tt, tbeg = blockIdx.x >> 1, tstep = gridDim.x >> 1;
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0, issued = 0, par = 0;
+            bool ok = true;
+            const uint32_t bytes = 2u * (kAStage + p.BN / 2 * 128);      // of both CTAs
+            for (int t = tbeg; t < total && ok; t += tstep) {
+                int wt, tt;
+                tile_of(p, t, wt, tt);
+                const int f0 = (wt * 2 + (int)rank) * kF, row = tt * p.BN + (int)rank * (p.BN / 2);
+                for (int kb = 0; kb < p.nkb; ++kb) {
+                    if (!mbar_wait(&empty[s], ph ^ 1, s_abort, p.wait_limit)) { ok = false; break; }
+                    // both CTAs' loads complete on the even CTA's barrier, which arrives once
+                    const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+                    unsigned char* a = sA + s * kAStage;
+                    if (ACT == MOE_ACT_SWIGLU) {
+                        for (int q = 0; q < 4; ++q) tma_load_3d_pair(a + q * 4096, &tmA, kb * kBK, f0 + 16 * q, 0, fb);
+                    } else {
+                        tma_load_2d_pair(a, &tmA, kb * kBK, f0, fb);
+                    }
+                    tma_load_2d_pair(sB + s * kAStage, &tmB, kb * kBK, row, fb);
+                    issued |= 1u << s;
+                    par = (par & ~(1u << s)) | (ph << s);
+                    if (++s == kPairStages) { s = 0; ph ^= 1; }
+                }
+            }
+            if (!ok) {
+                report_error(p.err, kErrWaitExpired);
+                *s_abort = 1;
+            }
+            if (rank == 0)                       // counts the odd CTA's bytes too
+                for (int q = 0; q < kPairStages; ++q)
+                    if (issued >> q & 1u) mbar_wait(&full[q], par >> q & 1u, nullptr, p.wait_limit);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int s = 0, it = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            const uint32_t idesc = idesc_bf16(256, p.BN);
+            for (int t = tbeg; t < total && ok; t += tstep, ++it) {
+                const int buf = it & 1;
+                if (!mbar_wait(&tempty[buf], ((it >> 1) & 1) ^ 1, s_abort, p.wait_limit)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d = tmem + buf * 256;
+                for (int kb = 0; kb < p.nkb; ++kb) {
+                    if (!mbar_wait(&full[s], ph, s_abort, p.wait_limit)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t ad = sdesc_sw128(smem_u32(sA + s * kAStage));
+                    const uint64_t bd = sdesc_sw128(smem_u32(sB + s * kAStage));
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        umma_bf16_pair(d, ad + uint64_t(kk * 2), bd + uint64_t(kk * 2), idesc, kb != 0 || kk != 0);
+                    umma_commit_pair_both(&empty[s]);
+                    if (++s == kPairStages) { s = 0; ph ^= 1; }
+                }
+                if (!ok) break;
+                umma_commit_pair_both(&tfull[buf]);
+            }
+            if (!ok) {
+                report_error(p.err, kErrWaitExpired);
+                *s_abort = 1;
+            }
+            umma_commit_pair_local(drain);
+            mbar_wait(drain, 0, nullptr, p.wait_limit);
+        }
+        __syncwarp();
+    } else {
+        const int sub = warp & 3, row = 32 * sub + lane;
+        int it = 0;
+        bool dead = false;
+        for (int t = tbeg; t < total; t += tstep, ++it) {
+            int wt, tt;
+            tile_of(p, t, wt, tt);
+            const int buf = it & 1, f = feature_of<ACT>((wt * 2 + (int)rank) * kF, row);
+            float b0, b1;
+            bias_of<ACT>(p, f, b0, b1);
+            if (!dead) {
+                const bool ok = mbar_wait(&tfull[buf], (it >> 1) & 1, s_abort, p.wait_limit);
+                if (__any_sync(0xffffffffu, !ok)) {
+                    if (lane == 0) report_error(p.err, kErrWaitExpired);
+                    *s_abort = 1;
+                    dead = true;
+                }
+            }
+            tc_fence_after();
+            if (!dead) {
+                const uint32_t tb = tmem + (uint32_t(32 * sub) << 16) + buf * 256;
+                const int nc = min(p.BN, p.M - tt * p.BN);
+                for (int c = 0; c < nc; c += 16) {
+                    float v[16];
+                    tmem_ld16(tb + c, v);
+                    emit<ACT, 16>(p, v, f, tt * p.BN + c, b0, b1);
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (rank != 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
+                else mbar_arrive(&tempty[buf]);
+            }
+        }
+    }
+    __syncthreads();
+    cluster_sync();                              // the pair's MMAs and both epilogues are done with TMEM
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+MOE_DEV float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(kLinThreads)
+    k_linear_split(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, LinParams p) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* sm =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int S = p.stages, bstage = p.BN * 128;
+    unsigned char* sA = sm;
+    unsigned char* sB = sm + S * kAStage;
+    __shared__ uint64_t full[kMaxStage], empty[kMaxStage], done;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    constexpr int kF = ACT == MOE_ACT_SWIGLU ? 64 : 128;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = p.ks > 1 ? (int)cluster_ctarank() : 0;
+    const int tile = blockIdx.x / p.ks, tt = tile / p.n_wt, wt = tile - tt * p.n_wt;
+    const int kb0 = rank * p.nkb / p.ks, kb1 = (rank + 1) * p.nkb / p.ks;
+    const int cols = p.BN <= 32 ? 32 : p.BN <= 64 ? 64 : p.BN <= 128 ? 128 : 256;   // TMEM columns
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(&done, 1);
+        s_abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(&s_tmem, cols);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    pdl_wait();
+    pdl_trigger();
+    const int f0 = wt * kF;
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0, issued = 0, par = 0;
+            bool ok = true;
+            const uint64_t pol = policy_evict_first();           // weights of a single token tile are read once
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(&empty[s], ph ^ 1, &s_abort, p.wait_limit)) { ok = false; break; }
+                mbar_arrive_expect_tx(&full[s], kAStage + bstage);
+                unsigned char* a = sA + s * kAStage;
+                if (ACT == MOE_ACT_SWIGLU) {
+                    for (int q = 0; q < 4; ++q) tma_load_3d(a + q * 4096, &tmA, kb * kBK, f0 + 16 * q, 0, &full[s]);
+                } else if (p.n_tt == 1) {
+                    tma_load_2d_hint(a, &tmA, kb * kBK, f0, &full[s], pol);
+                } else {
+                    tma_load_2d(a, &tmA, kb * kBK, f0, &full[s]);
+                }
+                tma_load_2d(sB + s * bstage, &tmB, kb * kBK, tt * p.BN, &full[s]);
+                issued |= 1u << s;
+                par = (par & ~(1u << s)) | (ph << s);
+                if (++s == S) { s = 0; ph ^= 1; }
+            }
+            if (!ok) {
+                report_error(p.err, kErrWaitExpired);
+                s_abort = 1;
+            }
+            for (int q = 0; q < S; ++q)
+                if (issued >> q & 1u) mbar_wait(&full[q], par >> q & 1u, nullptr, p.wait_limit);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            const uint32_t idesc = idesc_bf16(128, p.BN);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(&full[s], ph, &s_abort, p.wait_limit)) { ok = false; break; }
+                tc_fence_after();
+                const uint64_t ad = sdesc_sw128(smem_u32(sA + s * kAStage));
+                const uint64_t bd = sdesc_sw128(smem_u32(sB + s * bstage));
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk)
+                    umma_bf16(tmem, ad + uint64_t(kk * 2), bd + uint64_t(kk * 2), idesc, kb != kb0 || kk != 0);
+                umma_commit(&empty[s]);
+                if (++s == S) { s = 0; ph ^= 1; }
+            }
+            if (!ok) {
+                report_error(p.err, kErrWaitExpired);
+                s_abort = 1;
+            }
+            umma_commit(&done);
+        }
+        __syncwarp();
+    }
+    // The accumulator is complete, and with it every load has been consumed.
+    const bool ok = mbar_wait(&done, 0, nullptr, p.wait_limit);
+    if (!ok) s_abort = 1;
+    __syncthreads();
+    tc_fence_after();
+    const bool dead = s_abort != 0;
+    if (dead && threadIdx.x == 0) report_error(p.err, kErrWaitExpired);
+    const int sub = warp & 3, row = 32 * sub + lane;
+    const int f = feature_of<ACT>(f0, row), t0 = tt * p.BN;
+    const int nc = min(p.BN, p.M - t0);          // tokens of this tile
+    float b0, b1;
+    bias_of<ACT>(p, f, b0, b1);
+    const uint32_t tb = tmem + (uint32_t(32 * sub) << 16);
+    if (p.ks == 1) {
+        if (warp >= 2 && !dead)
+            for (int c = 0; c < nc; c += 16) {
+                float v[16];
+                tmem_ld16(tb + c, v);
+                emit<ACT, 16>(p, v, f, t0 + c, b0, b1);
+                __syncwarp();
+            }
+    } else {
+        float* part = reinterpret_cast<float*>(sm);              // [BN][128], over the stages
+        if (warp >= 2)
+            for (int c = 0; c < nc; c += 16) {
+                float v[16];
+                tmem_ld16(tb + c, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) part[(c + i) * 128 + row] = v[i];
+            }
+        cluster_sync();
+        if (warp >= 2 && !dead) {
+            const uint32_t mine = smem_u32(part);
+            for (int c = rank * 2; c < nc; c += p.ks * 2) {      // two columns at a time, dealt out to the ranks
+                float v[2] = {0.0f, 0.0f};
+                for (int r = 0; r < p.ks; ++r) {
+                    const uint32_t a = mapa_shared(mine + (c * 128 + row) * 4, r);
+                    v[0] += ld_cluster_f32(a);
+                    v[1] += ld_cluster_f32(a + 512);
+                }
+                emit<ACT, 2>(p, v, f, t0 + c, b0, b1);
+                __syncwarp();
+            }
+        }
+        cluster_sync();                          // nobody leaves while its sums are read
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, cols);
+    }
+}
+
+// ---------------------------------------------------------------------------- host side
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* q = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r) ==
+                cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(q);
+    });
+    return fn;
+}
+
+// bf16 rows in the 128-byte swizzle; halves > 1 adds a third dimension of that
+// many row blocks, `rows` rows apart.
+cudaError_t make_map(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t ld, uint32_t box_rows,
+                     uint32_t halves) {
+    EncodeFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {K, rows, halves}, strides[2] = {ld * 2, rows * ld * 2};
+    const cuuint32_t box[3] = {kBK, box_rows, halves}, ones[3] = {1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, halves > 1 ? 3 : 2, const_cast<void*>(base), dims,
+                           strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+struct LinCall {
+    const void *x, *w;
+    long long ldx, ldw;
+    int K;
+};
+
+template <int ACT>
+cudaError_t maps(const LinCall& c, const LinParams& p, uint32_t b_rows, CUtensorMap* ta, CUtensorMap* tb) {
+    cudaError_t e = ACT == MOE_ACT_SWIGLU ? make_map(ta, c.w, c.K, p.N, c.ldw, 16, 2)
+                                          : make_map(ta, c.w, c.K, p.N, c.ldw, 128, 1);
+    return e != cudaSuccess ? e : make_map(tb, c.x, c.K, p.M, c.ldx, b_rows, 1);
+}
+
+// Tokens of a pair tile: the width that finishes all tiles soonest, when a
+// tile costs its width plus a fixed part.
+int pick_bn(int M, int n_wt, int pairs) {
+    int best = 256;
+    long long cost = -1;
+    for (int bn = 256; bn >= 32; bn -= 16) {
+        const long long tiles = (long long)n_wt * ((M + bn - 1) / bn);
+        const long long c = (tiles + pairs - 1) / pairs * (bn + 16);
+        if (cost < 0 || c < cost) {
+            cost = c;
+            best = bn;
+        }
+    }
+    return best;
+}
+
+template <int ACT>
+cudaError_t run_linear(const LinCall& c, LinParams p, cudaStream_t s) {
+    const DeviceInfo& di = device_info();
+    constexpr int kF = ACT == MOE_ACT_SWIGLU ? 64 : 128;
+    const int pairs = di.sm_count / 2;
+    CUtensorMap ta, tb;
+    cudaError_t e;
+    p.nkb = (c.K + kBK - 1) / kBK;
+    const int wt2 = (p.N + 2 * kF - 1) / (2 * kF), bn2 = pick_bn(p.M, wt2, pairs);
+    const long long tiles2 = (long long)wt2 * ((p.M + bn2 - 1) / bn2);
+    // Pair tiles when they fill half of the SMs or more.
+    if (p.M > 64 && tiles2 * 2 > pairs) {
+        p.BN = bn2;
+        p.n_wt = wt2;
+        p.n_tt = (p.M + bn2 - 1) / bn2;
+        if ((e = maps<ACT>(c, p, bn2 / 2, &ta, &tb)) != cudaSuccess) return e;
+        auto kern = k_linear_pair<ACT>;
+        if ((e = ensure_smem(kern, kPairSmem)) != cudaSuccess) return e;
+        const int grid = (int)std::min<long long>(tiles2, pairs) * 2;
+        return launch_k_pair(kern, dim3(grid), dim3(kLinThreads), kPairSmem, s, true, ta, tb, p);
+    }
+    p.BN = std::min(128, (p.M + 15) / 16 * 16);
+    p.n_wt = (p.N + kF - 1) / kF;
+    p.n_tt = (p.M + p.BN - 1) / p.BN;
+    const long long tiles = (long long)p.n_wt * p.n_tt;
+    p.ks = 1;
+    while (p.ks < 8 && tiles * p.ks * 2 <= 2 * di.sm_count && p.nkb >= p.ks * 4) p.ks *= 2;
+    const int stage = kAStage + p.BN * 128;
+    p.stages = std::max(2, std::min(std::min(kMaxStage, 100 * 1024 / stage), (p.nkb + p.ks - 1) / p.ks));
+    const size_t smem = std::max((size_t)p.stages * stage, (size_t)p.BN * 512) + 1024;
+    if ((e = maps<ACT>(c, p, p.BN, &ta, &tb)) != cudaSuccess) return e;
+    auto kern = k_linear_split<ACT>;
+    if ((e = ensure_smem(kern, smem)) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * p.ks));
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.ks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.ks > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
+}
+
+moe_status refuse(moe_status st, const char* msg) {
+    set_last_error(msg);
+    return st;
+}
+bool misaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_linear(const void* x, const void* w, const float* bias, const void* residual,
+                                 const moe_linear_dims* d, const moe_linear_cfg* cfg, void* y, moe_stream_t stream) {
+    if (!d || !cfg) return refuse(MOE_ERR_NULL, "dims or cfg is NULL");
+    if (d->M < 0 || d->N < 1 || d->K < 1) return refuse(MOE_ERR_SHAPE, "moe_linear: need M >= 0, N >= 1, K >= 1");
+    constexpr int kMost = 1 << 24;
+    if (d->M > kMost || d->N > kMost || d->K > kMost) return refuse(MOE_ERR_SHAPE, "moe_linear: a size above 2^24");
+    if (cfg->act != MOE_ACT_NONE && cfg->act != MOE_ACT_RELU2 && cfg->act != MOE_ACT_SWIGLU)
+        return refuse(MOE_ERR_UNSUPPORTED, "moe_linear: activation");
+    if ((cfg->res_f32 | cfg->y_f32) & ~1) return refuse(MOE_ERR_UNSUPPORTED, "moe_linear: res_f32 and y_f32 are 0 or 1");
+    if (!(cfg->swiglu_limit >= 0.0f) || cfg->swiglu_limit > 3.0e38f)
+        return refuse(MOE_ERR_SHAPE, "swiglu_limit must be finite and >= 0 (0 = off)");
+    const long long ldx = d->ldx ? d->ldx : d->K, ldw = d->ldw ? d->ldw : d->K;
+    const long long ldr = d->ldr ? d->ldr : d->N, ldy = d->ldy ? d->ldy : d->N;
+    constexpr long long kMostLd = 1ll << 31;
+    if (ldx < d->K || ldw < d->K || ldr < d->N || ldy < d->N || ldx > kMostLd || ldw > kMostLd || ldr > kMostLd ||
+        ldy > kMostLd)
+        return refuse(MOE_ERR_SHAPE, "moe_linear: a row stride below the row length (or above 2^31)");
+    if (ldx % 8 || ldw % 8) return refuse(MOE_ERR_ALIGN, "moe_linear: row strides of x and w must be multiples of 8 elements");
+    if (d->M == 0) return set_last_launch_count(0), MOE_OK;
+    if (!x || !w || !y) return refuse(MOE_ERR_NULL, "x, w or y is NULL");
+    if (misaligned(x, 16) || misaligned(w, 16)) return refuse(MOE_ERR_ALIGN, "x or w not 16-byte aligned");
+    if (misaligned(bias, 4) || misaligned(residual, cfg->res_f32 ? 4 : 2) || misaligned(y, cfg->y_f32 ? 4 : 2))
+        return refuse(MOE_ERR_ALIGN, "bias, residual or y not aligned to its elements");
+    LinCall c{x, w, ldx, ldw, d->K};
+    LinParams p{};
+    p.bias = bias;
+    p.residual = residual;
+    p.y = y;
+    p.ldr = ldr;
+    p.ldy = ldy;
+    p.M = d->M;
+    p.N = d->N;
+    p.res_f32 = cfg->res_f32;
+    p.y_f32 = cfg->y_f32;
+    p.limit = cfg->swiglu_limit;
+    p.wait_limit = sm100::kWaitLimit;
+    p.err = device_info().err_word;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = cfg->act == MOE_ACT_NONE    ? run_linear<MOE_ACT_NONE>(c, p, s)
+                          : cfg->act == MOE_ACT_RELU2 ? run_linear<MOE_ACT_RELU2>(c, p, s)
+                                                      : run_linear<MOE_ACT_SWIGLU>(c, p, s);
+    if (e != cudaSuccess) {
+        set_last_error(cudaGetErrorString(e));
+        return MOE_ERR_CUDA;
+    }
+    set_last_launch_count(1);
+    return MOE_OK;
+}
