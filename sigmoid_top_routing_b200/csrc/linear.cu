@@ -128,6 +128,20 @@ MOE_DEV void bias_of(const LinParams& p, int f, float& b0, float& b1) {
     }
 }
 
+// One lane of a converged warp.  Producer and MMA loops run on all 32 lanes with
+// warp-uniform values and only their TMA, MMA and commit instructions under this
+// predicate: inside an `if (lane == 0)` those instructions' operands are not
+// uniform to the compiler, which then issues them lane by lane (~40 cycles each;
+// a k-block of the pair kernel took 305 ns whatever its width).
+MOE_DEV bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+MOE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag, uint32_t limit) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit));
+}
+
 // 3D tiled load (SwiGLU weights: k, row, gate / up half).
 MOE_DEV void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
     asm volatile(
@@ -202,71 +216,75 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     pdl_trigger();
     const int total = p.n_wt * p.n_tt, tbeg = blockIdx.x >> 1, tstep = gridDim.x >> 1;
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0, issued = 0, par = 0;
-            bool ok = true;
-            const uint32_t bytes = 2u * (kAStage + p.BN / 2 * 128);      // of both CTAs
-            for (int t = tbeg; t < total && ok; t += tstep) {
-                int wt, tt;
-                tile_of(p, t, wt, tt);
-                const int f0 = (wt * 2 + (int)rank) * kF, row = tt * p.BN + (int)rank * (p.BN / 2);
-                for (int kb = 0; kb < p.nkb; ++kb) {
-                    if (!mbar_wait(&empty[s], ph ^ 1, s_abort, p.wait_limit)) { ok = false; break; }
+        int s = 0;
+        uint32_t ph = 0, issued = 0, par = 0;
+        bool ok = true;
+        const uint32_t bytes = 2u * (kAStage + p.BN / 2 * 128);          // of both CTAs
+        for (int t = tbeg; t < total && ok; t += tstep) {
+            int wt, tt;
+            tile_of(p, t, wt, tt);
+            const int f0 = (wt * 2 + (int)rank) * kF, row = tt * p.BN + (int)rank * (p.BN / 2);
+            for (int kb = 0; kb < p.nkb; ++kb) {
+                if (!warp_wait(&empty[s], ph ^ 1, s_abort, p.wait_limit)) { ok = false; break; }
+                if (elect_one()) {
                     // both CTAs' loads complete on the even CTA's barrier, which arrives once
                     const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
                     unsigned char* a = sA + s * kAStage;
                     if (ACT == MOE_ACT_SWIGLU) {
+#pragma unroll
                         for (int q = 0; q < 4; ++q) tma_load_3d_pair(a + q * 4096, &tmA, kb * kBK, f0 + 16 * q, 0, fb);
                     } else {
                         tma_load_2d_pair(a, &tmA, kb * kBK, f0, fb);
                     }
                     tma_load_2d_pair(sB + s * kAStage, &tmB, kb * kBK, row, fb);
-                    issued |= 1u << s;
-                    par = (par & ~(1u << s)) | (ph << s);
-                    if (++s == kPairStages) { s = 0; ph ^= 1; }
                 }
+                __syncwarp();
+                issued |= 1u << s;
+                par = (par & ~(1u << s)) | (ph << s);
+                if (++s == kPairStages) { s = 0; ph ^= 1; }
             }
-            if (!ok) {
-                report_error(p.err, kErrWaitExpired);
-                *s_abort = 1;
-            }
-            if (rank == 0)                       // counts the odd CTA's bytes too
-                for (int q = 0; q < kPairStages; ++q)
-                    if (issued >> q & 1u) mbar_wait(&full[q], par >> q & 1u, nullptr, p.wait_limit);
         }
-        __syncwarp();
+        if (!ok) {
+            if (lane == 0) report_error(p.err, kErrWaitExpired);
+            *s_abort = 1;
+        }
+        if (rank == 0)                           // counts the odd CTA's bytes too
+            for (int q = 0; q < kPairStages; ++q)
+                if (issued >> q & 1u) mbar_wait(&full[q], par >> q & 1u, nullptr, p.wait_limit);
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             int s = 0, it = 0;
             uint32_t ph = 0;
             bool ok = true;
             const uint32_t idesc = idesc_bf16(256, p.BN);
             for (int t = tbeg; t < total && ok; t += tstep, ++it) {
                 const int buf = it & 1;
-                if (!mbar_wait(&tempty[buf], ((it >> 1) & 1) ^ 1, s_abort, p.wait_limit)) { ok = false; break; }
+                if (!warp_wait(&tempty[buf], ((it >> 1) & 1) ^ 1, s_abort, p.wait_limit)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem + buf * 256;
                 for (int kb = 0; kb < p.nkb; ++kb) {
-                    if (!mbar_wait(&full[s], ph, s_abort, p.wait_limit)) { ok = false; break; }
+                    if (!warp_wait(&full[s], ph, s_abort, p.wait_limit)) { ok = false; break; }
                     tc_fence_after();
                     const uint64_t ad = sdesc_sw128(smem_u32(sA + s * kAStage));
                     const uint64_t bd = sdesc_sw128(smem_u32(sB + s * kAStage));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk)
-                        umma_bf16_pair(d, ad + uint64_t(kk * 2), bd + uint64_t(kk * 2), idesc, kb != 0 || kk != 0);
-                    umma_commit_pair_both(&empty[s]);
+                        for (int kk = 0; kk < kBK / 16; ++kk)
+                            umma_bf16_pair(d, ad + uint64_t(kk * 2), bd + uint64_t(kk * 2), idesc, kb != 0 || kk != 0);
+                        umma_commit_pair_both(&empty[s]);
+                        if (kb == p.nkb - 1) umma_commit_pair_both(&tfull[buf]);
+                    }
+                    __syncwarp();
                     if (++s == kPairStages) { s = 0; ph ^= 1; }
                 }
-                if (!ok) break;
-                umma_commit_pair_both(&tfull[buf]);
             }
             if (!ok) {
-                report_error(p.err, kErrWaitExpired);
+                if (lane == 0) report_error(p.err, kErrWaitExpired);
                 *s_abort = 1;
             }
-            umma_commit_pair_local(drain);
+            if (elect_one()) umma_commit_pair_local(drain);
+            __syncwarp();
             mbar_wait(drain, 0, nullptr, p.wait_limit);
         }
         __syncwarp();
@@ -362,16 +380,17 @@ __global__ void __launch_bounds__(kLinThreads)
     pdl_trigger();
     const int f0 = wt * kF;
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0, issued = 0, par = 0;
-            bool ok = true;
-            const uint64_t pol = policy_evict_first();           // weights of a single token tile are read once
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(&empty[s], ph ^ 1, &s_abort, p.wait_limit)) { ok = false; break; }
+        int s = 0;
+        uint32_t ph = 0, issued = 0, par = 0;
+        bool ok = true;
+        const uint64_t pol = policy_evict_first();               // weights of a single token tile are read once
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!warp_wait(&empty[s], ph ^ 1, &s_abort, p.wait_limit)) { ok = false; break; }
+            if (elect_one()) {
                 mbar_arrive_expect_tx(&full[s], kAStage + bstage);
                 unsigned char* a = sA + s * kAStage;
                 if (ACT == MOE_ACT_SWIGLU) {
+#pragma unroll
                     for (int q = 0; q < 4; ++q) tma_load_3d(a + q * 4096, &tmA, kb * kBK, f0 + 16 * q, 0, &full[s]);
                 } else if (p.n_tt == 1) {
                     tma_load_2d_hint(a, &tmA, kb * kBK, f0, &full[s], pol);
@@ -379,43 +398,46 @@ __global__ void __launch_bounds__(kLinThreads)
                     tma_load_2d(a, &tmA, kb * kBK, f0, &full[s]);
                 }
                 tma_load_2d(sB + s * bstage, &tmB, kb * kBK, tt * p.BN, &full[s]);
-                issued |= 1u << s;
-                par = (par & ~(1u << s)) | (ph << s);
-                if (++s == S) { s = 0; ph ^= 1; }
             }
-            if (!ok) {
-                report_error(p.err, kErrWaitExpired);
-                s_abort = 1;
-            }
-            for (int q = 0; q < S; ++q)
-                if (issued >> q & 1u) mbar_wait(&full[q], par >> q & 1u, nullptr, p.wait_limit);
+            __syncwarp();
+            issued |= 1u << s;
+            par = (par & ~(1u << s)) | (ph << s);
+            if (++s == S) { s = 0; ph ^= 1; }
         }
-        __syncwarp();
+        if (!ok) {
+            if (lane == 0) report_error(p.err, kErrWaitExpired);
+            s_abort = 1;
+        }
+        for (int q = 0; q < S; ++q)
+            if (issued >> q & 1u) mbar_wait(&full[q], par >> q & 1u, nullptr, p.wait_limit);
     } else if (warp == 1) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            const uint32_t idesc = idesc_bf16(128, p.BN);
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(&full[s], ph, &s_abort, p.wait_limit)) { ok = false; break; }
-                tc_fence_after();
-                const uint64_t ad = sdesc_sw128(smem_u32(sA + s * kAStage));
-                const uint64_t bd = sdesc_sw128(smem_u32(sB + s * bstage));
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        const uint32_t idesc = idesc_bf16(128, p.BN);
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!warp_wait(&full[s], ph, &s_abort, p.wait_limit)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t ad = sdesc_sw128(smem_u32(sA + s * kAStage));
+            const uint64_t bd = sdesc_sw128(smem_u32(sB + s * bstage));
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kBK / 16; ++kk)
                     umma_bf16(tmem, ad + uint64_t(kk * 2), bd + uint64_t(kk * 2), idesc, kb != kb0 || kk != 0);
                 umma_commit(&empty[s]);
-                if (++s == S) { s = 0; ph ^= 1; }
+                if (kb == kb1 - 1) umma_commit(&done);
             }
-            if (!ok) {
-                report_error(p.err, kErrWaitExpired);
-                s_abort = 1;
-            }
-            umma_commit(&done);
+            __syncwarp();
+            if (++s == S) { s = 0; ph ^= 1; }
         }
-        __syncwarp();
+        if (!ok) {
+            if (lane == 0) report_error(p.err, kErrWaitExpired);
+            s_abort = 1;
+            if (elect_one()) umma_commit(&done);                 // what was issued completes
+            __syncwarp();
+        }
     }
+    __syncwarp();
     // The accumulator is complete, and with it every load has been consumed.
     const bool ok = mbar_wait(&done, 0, nullptr, p.wait_limit);
     if (!ok) s_abort = 1;
