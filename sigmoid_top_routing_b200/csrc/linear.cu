@@ -59,18 +59,67 @@ struct LinParams {
     int* err;
 };
 
+// Residual values of NC consecutive tokens of one feature (the column at t0),
+// requested together; FULL: all of them exist.
+template <int NC, bool FULL>
+MOE_DEV void load_res(const LinParams& p, int f, int t0, int n, float (&q)[NC]) {
+    if (p.res_f32) {
+        const float* r = static_cast<const float*>(p.residual) + (size_t)t0 * p.ldr + f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            q[i] = FULL || i < n ? *r : 0.0f;
+            r += p.ldr;
+        }
+    } else {
+        const uint16_t* r = static_cast<const uint16_t*>(p.residual) + (size_t)t0 * p.ldr + f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            q[i] = __uint_as_float((FULL || i < n) ? (uint32_t)*r : 0u);   // widened in add_res
+            r += p.ldr;
+        }
+    }
+}
+template <int NC>
+MOE_DEV void add_res(const LinParams& p, const float (&q)[NC], float (&o)[NC]) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) o[i] += p.res_f32 ? q[i] : __uint_as_float(__float_as_uint(q[i]) << 16);
+}
+template <int NC, bool FULL>
+MOE_DEV void store_out(const LinParams& p, int f, int t0, int n, const float (&o)[NC]) {
+    if (p.y_f32) {
+        float* y = static_cast<float*>(p.y) + (size_t)t0 * p.ldy + f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            if (FULL || i < n) *y = o[i];
+            y += p.ldy;
+        }
+    } else {
+        uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)t0 * p.ldy + f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            if (FULL || i < n) *y = f2bf16(o[i]);
+            y += p.ldy;
+        }
+    }
+}
+
 // Epilogue of NC columns (tokens t0 .. t0 + NC - 1) of this lane's feature row.
 // f: the lane's feature (SwiGLU: the same for lanes l and l + 16).
 template <int ACT, int NC>
 MOE_DEV void emit(const LinParams& p, const float (&v)[NC], int f, int t0, float b0, float b1) {
     constexpr int C = ACT == MOE_ACT_SWIGLU ? NC / 2 : NC;       // columns this lane stores
     const int lane = threadIdx.x & 31;
-    float o[C];
-    int t = t0;
+    const int t = ACT == MOE_ACT_SWIGLU && lane >= 16 ? t0 + C : t0;
+    const int n = min(C, p.M - t);
+    const bool live = f < p.N, full = t0 + NC <= p.M;            // full: warp-uniform
+    float q[C], o[C];
+    if (p.residual && live) {                    // requested first: the activation hides some of the latency
+        if (full) load_res<C, true>(p, f, t, n, q);
+        else load_res<C, false>(p, f, t, n, q);
+    }
     if constexpr (ACT == MOE_ACT_SWIGLU) {
         // low lanes end up with gate and up of the first half of the columns, high lanes of the second
         const bool lo = lane < 16;
-        if (!lo) t += C;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const float other = __shfl_xor_sync(0xffffffffu, lo ? v[C + i] : v[i], 16);
@@ -82,35 +131,10 @@ MOE_DEV void emit(const LinParams& p, const float (&v)[NC], int f, int t0, float
 #pragma unroll
         for (int i = 0; i < C; ++i) o[i] = ACT == MOE_ACT_RELU2 ? act_relu2(v[i] + b0) : v[i] + b0;
     }
-    if (f >= p.N) return;
-    const int n = min(C, p.M - t);
-    if (p.residual) {
-        if (p.res_f32) {
-            const float* r = static_cast<const float*>(p.residual) + (size_t)t * p.ldr + f;
-            float q[C];
-#pragma unroll
-            for (int i = 0; i < C; ++i) q[i] = i < n ? r[(size_t)i * p.ldr] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < C; ++i) o[i] += q[i];
-        } else {
-            const uint16_t* r = static_cast<const uint16_t*>(p.residual) + (size_t)t * p.ldr + f;
-            uint16_t q[C];
-#pragma unroll
-            for (int i = 0; i < C; ++i) q[i] = i < n ? r[(size_t)i * p.ldr] : uint16_t(0);
-#pragma unroll
-            for (int i = 0; i < C; ++i) o[i] += bf16f(q[i]);
-        }
-    }
-    if (p.y_f32) {
-        float* y = static_cast<float*>(p.y) + (size_t)t * p.ldy + f;
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (i < n) y[(size_t)i * p.ldy] = o[i];
-    } else {
-        uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)t * p.ldy + f;
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (i < n) y[(size_t)i * p.ldy] = f2bf16(o[i]);
+    if (live) {
+        if (p.residual) add_res(p, q, o);
+        if (full) store_out<C, true>(p, f, t, n, o);
+        else store_out<C, false>(p, f, t, n, o);
     }
 }
 
