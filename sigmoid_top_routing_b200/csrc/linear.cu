@@ -42,7 +42,8 @@ using namespace sm100;
 
 constexpr int kBK = 64;                          // k per stage: one 128-byte swizzle row
 constexpr int kAStage = 128 * kBK * 2;           // 16 KB of weight rows per CTA
-constexpr int kLinThreads = 192;                 // producer, MMA issuer, 4 epilogue warps
+constexpr int kLinThreads = 192;                 // producer, MMA issuer, 4 epilogue warps (split)
+constexpr int kPairThreads = 320;                // ... 8 epilogue warps, two per TMEM quarter (pair)
 constexpr int kMaxStage = 8;
 
 struct LinParams {
@@ -125,7 +126,8 @@ MOE_DEV void emit(const LinParams& p, const float (&v)[NC], int f, int t0, float
             const float other = __shfl_xor_sync(0xffffffffu, lo ? v[C + i] : v[i], 16);
             float g = (lo ? v[i] : other) + b0, u = (lo ? other : v[C + i]) + b1;
             clamp_swiglu(g, u, p.limit);
-            o[i] = act_swiglu(g, u);
+            // bf16 results: exp and the quotient to ~2^-19, far below the store's 2^-8
+            o[i] = p.y_f32 ? act_swiglu(g, u) : __fdividef(g, 1.0f + __expf(-g)) * u;
         }
     } else {
 #pragma unroll
@@ -195,7 +197,7 @@ constexpr int kPairStages = 6;
 constexpr size_t kPairSmem = size_t(kPairStages) * 2 * kAStage + 1024 + 256;
 
 template <int ACT>
-__global__ void __launch_bounds__(kLinThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, LinParams p) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm =
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 8);
+            mbar_init(&tempty[b], 16);            // the epilogue warps of both CTAs
         }
         mbar_init(drain, 1);
         *s_abort = 0;
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if (!dead) {
                 const uint32_t tb = tmem + (uint32_t(32 * sub) << 16) + buf * 256;
                 const int nc = min(p.BN, p.M - tt * p.BN);
-                for (int c = 0; c < nc; c += 16) {
+                for (int c = warp < 6 ? 0 : 16; c < nc; c += 32) {
                     float v[16];
                     tmem_ld16(tb + c, v);
                     emit<ACT, 16>(p, v, f, tt * p.BN + c, b0, b1);
@@ -563,14 +565,15 @@ cudaError_t maps(const LinCall& c, const LinParams& p, uint32_t b_rows, CUtensor
     return e != cudaSuccess ? e : make_map(tb, c.x, c.K, p.M, c.ldx, b_rows, 1);
 }
 
-// Tokens of a pair tile: the width that finishes all tiles soonest, when a
-// tile costs its width plus a fixed part.
+// Tokens of a pair tile: the width that finishes all tiles soonest.  A k-block
+// of a tile measured 225-250 ns at 128 tokens and 295-370 ns at 256 (one tile
+// alone - all SMs busy), so a tile costs its width plus 160.
 int pick_bn(int M, int n_wt, int pairs) {
     int best = 256;
     long long cost = -1;
     for (int bn = 256; bn >= 32; bn -= 16) {
         const long long tiles = (long long)n_wt * ((M + bn - 1) / bn);
-        const long long c = (tiles + pairs - 1) / pairs * (bn + 16);
+        const long long c = (tiles + pairs - 1) / pairs * (bn + 160);
         if (cost < 0 || c < cost) {
             cost = c;
             best = bn;
@@ -598,7 +601,7 @@ cudaError_t run_linear(const LinCall& c, LinParams p, cudaStream_t s) {
         auto kern = k_linear_pair<ACT>;
         if ((e = ensure_smem(kern, kPairSmem)) != cudaSuccess) return e;
         const int grid = (int)std::min<long long>(tiles2, pairs) * 2;
-        return launch_k_pair(kern, dim3(grid), dim3(kLinThreads), kPairSmem, s, true, ta, tb, p);
+        return launch_k_pair(kern, dim3(grid), dim3(kPairThreads), kPairSmem, s, true, ta, tb, p);
     }
     p.BN = std::min(128, (p.M + 15) / 16 * 16);
     p.n_wt = (p.N + kF - 1) / kF;
