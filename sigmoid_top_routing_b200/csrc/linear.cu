@@ -16,7 +16,7 @@
 //   k_linear_pair   persistent, 256 x BN tiles on SM pairs (cta_group::2), for
 //                   products with enough tiles to fill the SMs.  Each CTA loads
 //                   its 128 weight rows and half of the token rows per k-block
-//                   of 64 into a ring of 6 stages; two TMEM accumulators let the
+//                   of 64 into a ring of stages; two TMEM accumulators let the
 //                   epilogue of one tile overlap the next one's MMAs.
 //   k_linear_split  one 128 x BN tile per cluster of ks CTAs that share its K,
 //                   for few tokens or small products: partial sums meet through
@@ -45,6 +45,7 @@ constexpr int kAStage = 128 * kBK * 2;           // 16 KB of weight rows per CTA
 constexpr int kLinThreads = 192;                 // producer, MMA issuer, 4 epilogue warps (split)
 constexpr int kPairThreads = 320;                // ... 8 epilogue warps, two per TMEM quarter (pair)
 constexpr int kMaxStage = 8;
+constexpr int kMaxKs = 8;                        // CTAs that share a tile's K
 
 struct LinParams {
     const float* bias;
@@ -193,8 +194,12 @@ MOE_DEV void tile_of(const LinParams& p, int t, int& wt, int& tt) {
     wt = g * 8 + r - tt * gw;
 }
 
-constexpr int kPairStages = 6;
-constexpr size_t kPairSmem = size_t(kPairStages) * 2 * kAStage + 1024 + 256;
+// Pair stages hold two k-blocks: a round of the pipeline (wait, issue, commit)
+// costs ~200 ns whatever it moves, which bounded narrow tiles at 64 k a round.
+constexpr int kPairA = 2 * kAStage;              // 32 KB of weight rows per CTA
+constexpr int kPairRing = 192 * 1024;
+constexpr int kPairMaxStages = 5;
+constexpr size_t kPairSmem = size_t(kPairRing) + 1024 + 256;
 
 template <int ACT>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -203,10 +208,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     unsigned char* sm =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* sA = sm;
-    unsigned char* sB = sm + kPairStages * kAStage;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sB + kPairStages * kAStage);
-    uint64_t* empty = full + kPairStages;
-    uint64_t* tfull = empty + kPairStages;
+    const int S = p.stages, bstage = p.BN * 128;             // two blocks of BN / 2 token rows
+    unsigned char* sB = sm + S * kPairA;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + kPairRing);
+    uint64_t* empty = full + kPairMaxStages;
+    uint64_t* tfull = empty + kPairMaxStages;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPairStages; ++s) {
+        for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -245,30 +251,34 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         int s = 0;
         uint32_t ph = 0, issued = 0, par = 0;
         bool ok = true;
-        const uint32_t bytes = 2u * (kAStage + p.BN / 2 * 128);          // of both CTAs
+        const uint32_t bytes = 2u * (kPairA + bstage);                   // of both CTAs
         for (int t = tbeg; t < total && ok; t += tstep) {
             int wt, tt;
             tile_of(p, t, wt, tt);
             const int f0 = (wt * 2 + (int)rank) * kF, row = tt * p.BN + (int)rank * (p.BN / 2);
-            for (int kb = 0; kb < p.nkb; ++kb) {
+            for (int kb = 0; kb < p.nkb; kb += 2) {      // k past the end is zero-filled
                 if (!warp_wait(&empty[s], ph ^ 1, s_abort, p.wait_limit)) { ok = false; break; }
                 if (elect_one()) {
                     // both CTAs' loads complete on the even CTA's barrier, which arrives once
                     const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-                    unsigned char* a = sA + s * kAStage;
-                    if (ACT == MOE_ACT_SWIGLU) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) tma_load_3d_pair(a + q * 4096, &tmA, kb * kBK, f0 + 16 * q, 0, fb);
-                    } else {
-                        tma_load_2d_pair(a, &tmA, kb * kBK, f0, fb);
+                    for (int h = 0; h < 2; ++h) {
+                        unsigned char* a = sA + s * kPairA + h * kAStage;
+                        const int x = (kb + h) * kBK;
+                        if (ACT == MOE_ACT_SWIGLU) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) tma_load_3d_pair(a + q * 4096, &tmA, x, f0 + 16 * q, 0, fb);
+                        } else {
+                            tma_load_2d_pair(a, &tmA, x, f0, fb);
+                        }
+                        tma_load_2d_pair(sB + s * bstage + h * (bstage / 2), &tmB, x, row, fb);
                     }
-                    tma_load_2d_pair(sB + s * kAStage, &tmB, kb * kBK, row, fb);
                 }
                 __syncwarp();
                 issued |= 1u << s;
                 par = (par & ~(1u << s)) | (ph << s);
-                if (++s == kPairStages) { s = 0; ph ^= 1; }
+                if (++s == S) { s = 0; ph ^= 1; }
             }
         }
         if (!ok) {
@@ -276,7 +286,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             *s_abort = 1;
         }
         if (rank == 0)                           // counts the odd CTA's bytes too
-            for (int q = 0; q < kPairStages; ++q)
+            for (int q = 0; q < S; ++q)
                 if (issued >> q & 1u) mbar_wait(&full[q], par >> q & 1u, nullptr, p.wait_limit);
     } else if (warp == 1) {
         if (rank == 0) {
@@ -289,20 +299,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (!warp_wait(&tempty[buf], ((it >> 1) & 1) ^ 1, s_abort, p.wait_limit)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem + buf * 256;
-                for (int kb = 0; kb < p.nkb; ++kb) {
+                for (int kb = 0; kb < p.nkb; kb += 2) {
                     if (!warp_wait(&full[s], ph, s_abort, p.wait_limit)) { ok = false; break; }
                     tc_fence_after();
-                    const uint64_t ad = sdesc_sw128(smem_u32(sA + s * kAStage));
-                    const uint64_t bd = sdesc_sw128(smem_u32(sB + s * kAStage));
+                    const uint64_t ad = sdesc_sw128(smem_u32(sA + s * kPairA));
+                    const uint64_t bd = sdesc_sw128(smem_u32(sB + s * bstage));
+                    const uint64_t ad2 = ad + (kAStage >> 4), bd2 = bd + uint64_t(bstage >> 5);
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kBK / 16; ++kk)
                             umma_bf16_pair(d, ad + uint64_t(kk * 2), bd + uint64_t(kk * 2), idesc, kb != 0 || kk != 0);
+                        if (kb + 1 < p.nkb) {
+#pragma unroll
+                            for (int kk = 0; kk < kBK / 16; ++kk)
+                                umma_bf16_pair(d, ad2 + uint64_t(kk * 2), bd2 + uint64_t(kk * 2), idesc, true);
+                        }
                         umma_commit_pair_both(&empty[s]);
-                        if (kb == p.nkb - 1) umma_commit_pair_both(&tfull[buf]);
+                        if (kb + 2 >= p.nkb) umma_commit_pair_both(&tfull[buf]);
                     }
                     __syncwarp();
-                    if (++s == kPairStages) { s = 0; ph ^= 1; }
+                    if (++s == S) { s = 0; ph ^= 1; }
                 }
             }
             if (!ok) {
@@ -361,7 +377,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
 MOE_DEV float ld_cluster_f32(uint32_t addr) {
     float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
 
@@ -496,15 +512,24 @@ __global__ void __launch_bounds__(kLinThreads)
             }
         cluster_sync();
         if (warp >= 2 && !dead) {
+            // four columns at a time, dealt out to the ranks; all ranks' values are requested at once
             const uint32_t mine = smem_u32(part);
-            for (int c = rank * 2; c < nc; c += p.ks * 2) {      // two columns at a time, dealt out to the ranks
-                float v[2] = {0.0f, 0.0f};
-                for (int r = 0; r < p.ks; ++r) {
-                    const uint32_t a = mapa_shared(mine + (c * 128 + row) * 4, r);
-                    v[0] += ld_cluster_f32(a);
-                    v[1] += ld_cluster_f32(a + 512);
-                }
-                emit<ACT, 2>(p, v, f, t0 + c, b0, b1);
+            for (int c = rank * 4; c < nc; c += p.ks * 4) {
+                float q[kMaxKs][4], v[4] = {};
+#pragma unroll
+                for (int r = 0; r < kMaxKs; ++r)
+                    if (r < p.ks) {
+                        const uint32_t a = mapa_shared(mine + (c * 128 + row) * 4, r);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) q[r][i] = ld_cluster_f32(a + i * 512);
+                    }
+#pragma unroll
+                for (int r = 0; r < kMaxKs; ++r)
+                    if (r < p.ks) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] += q[r][i];
+                    }
+                emit<ACT, 4>(p, v, f, t0 + c, b0, b1);
                 __syncwarp();
             }
         }
@@ -597,6 +622,7 @@ cudaError_t run_linear(const LinCall& c, LinParams p, cudaStream_t s) {
         p.BN = bn2;
         p.n_wt = wt2;
         p.n_tt = (p.M + bn2 - 1) / bn2;
+        p.stages = std::min(kPairMaxStages, kPairRing / (kPairA + bn2 * 128));
         if ((e = maps<ACT>(c, p, bn2 / 2, &ta, &tb)) != cudaSuccess) return e;
         auto kern = k_linear_pair<ACT>;
         if ((e = ensure_smem(kern, kPairSmem)) != cudaSuccess) return e;
@@ -608,7 +634,7 @@ cudaError_t run_linear(const LinCall& c, LinParams p, cudaStream_t s) {
     p.n_tt = (p.M + p.BN - 1) / p.BN;
     const long long tiles = (long long)p.n_wt * p.n_tt;
     p.ks = 1;
-    while (p.ks < 8 && tiles * p.ks * 2 <= 2 * di.sm_count && p.nkb >= p.ks * 4) p.ks *= 2;
+    while (p.ks < kMaxKs && tiles * p.ks * 2 <= 2 * di.sm_count && p.nkb >= p.ks * 4) p.ks *= 2;
     const int stage = kAStage + p.BN * 128;
     p.stages = std::max(2, std::min(std::min(kMaxStage, 100 * 1024 / stage), (p.nkb + p.ks - 1) / p.ks));
     const size_t smem = std::max((size_t)p.stages * stage, (size_t)p.BN * 512) + 1024;
