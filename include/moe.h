@@ -329,6 +329,21 @@ typedef struct {
     float eps, router_scale, out_scale;
     moe_router_cfg router;
 } moe_layer;
+/* moe_decode in two parts, for a program that calls one layer step after step:
+ * moe_decode_prepare checks the layer and the sizes and describes the weights
+ * to the hardware once (on the current device, for exactly d->T tokens);
+ * moe_decode_run is then little more than a launch.  A plan is plain host
+ * memory: copy it, keep it as long as the layer's tensors stay where they are
+ * (new values in them count from the next call on), share it between threads.
+ * moe_decode is prepare and run.  A run on another device than the plan's is
+ * MOE_ERR_UNSUPPORTED. */
+typedef struct {
+    uint64_t opaque[192];
+} moe_decode_plan;
+MOE_API moe_status moe_decode_prepare(const moe_layer* L, const moe_dims* d, moe_decode_plan* plan);
+MOE_API moe_status moe_decode_run(const moe_decode_plan* plan, const void* x, const float* logits,
+                                  const void* residual, int32_t* topk_idx, float* topk_w, void* y, void* ws,
+                                  size_t ws_bytes, moe_stream_t stream);
 MOE_API size_t moe_decode_workspace_bytes(const moe_dims* d, int32_t Is);
 MOE_API moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void* x, const float* logits,
                               const void* residual, int32_t* topk_idx, float* topk_w, void* y, void* ws,

@@ -62,6 +62,10 @@ class moe_layer(ctypes.Structure):
                 ("router", moe_router_cfg)]
 
 
+class moe_decode_plan(ctypes.Structure):
+    _fields_ = [("opaque", ctypes.c_uint64 * 192)]
+
+
 class moe_linear_dims(ctypes.Structure):
     _fields_ = [("M", c_int32), ("N", c_int32), ("K", c_int32),
                 ("ldx", c_int64), ("ldw", c_int64), ("ldr", c_int64), ("ldy", c_int64)]
@@ -102,6 +106,9 @@ PROTOTYPES = {
     "moe_linear": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, POINTER(moe_linear_dims), POINTER(moe_linear_cfg),
                              c_void_p, c_void_p]),
     "moe_decode_workspace_bytes": (c_size_t, [POINTER(moe_dims), c_int32]),
+    "moe_decode_prepare": (c_int32, [POINTER(moe_layer), POINTER(moe_dims), POINTER(moe_decode_plan)]),
+    "moe_decode_run": (c_int32, [POINTER(moe_decode_plan), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                 c_void_p, c_size_t, c_void_p]),
     "moe_decode": (c_int32, [POINTER(moe_layer), POINTER(moe_dims), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                              c_void_p, c_void_p, c_size_t, c_void_p]),
     "moe_forward_host": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, POINTER(moe_dims), c_float,

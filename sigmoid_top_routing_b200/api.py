@@ -45,6 +45,12 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _stream_on(stream, device: int) -> int:
+    """_stream for the calls whose host time counts: the device's current stream
+    without building a torch.cuda.Stream object (3 us)."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
 @dataclasses.dataclass
 class ExpertWeights:
     """Device tensors of the experts (layouts as in include/moe.h)."""
@@ -238,9 +244,12 @@ def moe_forward_host(x_host: torch.Tensor, x_dev, W: ExpertWeights, w_router, ex
 _LINEAR_ACT = {"none": abi.MOE_ACT_NONE, "relu2": abi.MOE_ACT_RELU2, "swiglu": abi.MOE_ACT_SWIGLU}
 
 
+_BF16, _FP32, _OUT = (torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32)
+
+
 def _rows(name: str, t: torch.Tensor, rows: int, cols: int, dtypes, device) -> int:
     """Row stride of a (rows, cols) matrix with unit column stride, or ValueError."""
-    if t.device != device or t.dtype not in dtypes or t.dim() != 2 or tuple(t.shape) != (rows, cols):
+    if t.device != device or t.dtype not in dtypes or t.shape != (rows, cols):
         raise ValueError(f"{name}: expected ({rows}, {cols}) of {dtypes[0]} on {device}, got {tuple(t.shape)} of "
                          f"{t.dtype} on {t.device}")
     s0, s1 = t.stride()
@@ -259,33 +268,42 @@ def moe_linear(x, w, bias=None, residual=None, *, act: str = "none", swiglu_limi
     if not x.is_cuda or x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w: expected CUDA matrices")
     dev, (M, K), rows = x.device, x.shape, w.shape[0]
-    if act not in _LINEAR_ACT:
+    code = _LINEAR_ACT.get(act)
+    if code is None:
         raise ValueError(f"act: expected one of {sorted(_LINEAR_ACT)}, got {act!r}")
     if act == "swiglu" and rows % 2:
         raise ValueError("w: swiglu needs an even number of rows (gate, then up)")
     N = rows // 2 if act == "swiglu" else rows
-    ldx = _rows("x", x, M, K, (torch.bfloat16,), dev)
-    ldw = _rows("w", w, rows, K, (torch.bfloat16,), dev)
-    _want("bias", bias, (rows,), (torch.float32,), dev)
-    out = (torch.bfloat16, torch.float32)
-    ldr = _rows("residual", residual, M, N, out, dev) if residual is not None else N
+    ldx = _rows("x", x, M, K, _BF16, dev)
+    ldw = _rows("w", w, rows, K, _BF16, dev)
+    bias_p = res_p = None
+    ldr, res_f32 = N, False
+    if bias is not None:
+        _want("bias", bias, (rows,), _FP32, dev)
+        bias_p = bias.data_ptr()
+    if residual is not None:
+        ldr = _rows("residual", residual, M, N, _OUT, dev)
+        res_p, res_f32 = residual.data_ptr(), residual.dtype is torch.float32
     if y is None:
         y = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
-    elif out_dtype is not None and y.dtype != out_dtype:
-        raise ValueError(f"y is {y.dtype}, out_dtype is {out_dtype}")
-    ldy = _rows("y", y, M, N, out, dev)
+        if y.dtype not in _OUT:
+            raise ValueError(f"out_dtype: expected bfloat16 or float32, got {out_dtype}")
+        ldy = N
+    else:
+        if out_dtype is not None and y.dtype != out_dtype:
+            raise ValueError(f"y is {y.dtype}, out_dtype is {out_dtype}")
+        ldy = _rows("y", y, M, N, _OUT, dev)
     d = abi.moe_linear_dims(M, N, K, ldx, ldw, ldr, ldy)
-    cfg = abi.moe_linear_cfg(_LINEAR_ACT[act], residual is not None and residual.dtype == torch.float32,
-                             y.dtype == torch.float32, swiglu_limit)
+    cfg = abi.moe_linear_cfg(code, res_f32, y.dtype is torch.float32, swiglu_limit)
+    args = (x.data_ptr(), w.data_ptr(), bias_p, res_p, ctypes.byref(d), ctypes.byref(cfg), y.data_ptr(),
+            _stream_on(stream, dev.index))
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
-            return _linear(x, w, bias, residual, d, cfg, y, stream)
-    return _linear(x, w, bias, residual, d, cfg, y, stream)
-
-
-def _linear(x, w, bias, residual, d, cfg, y, stream):
-    check(load().moe_linear(x.data_ptr(), w.data_ptr(), _ptr(bias), None if residual is None else residual.data_ptr(),
-                            ctypes.byref(d), ctypes.byref(cfg), y.data_ptr(), _stream(stream)), "moe_linear")
+            st = load().moe_linear(*args)
+    else:
+        st = load().moe_linear(*args)
+    if st:
+        check(st, "moe_linear")
     return y
 
 
@@ -297,9 +315,9 @@ def _want(name: str, t: Optional[torch.Tensor], shape, dtypes, device) -> None:
     """Refuse a tensor that the library would read with another shape or type."""
     if t is None:
         return
-    if not t.is_cuda or t.device != device:
+    if t.device != device:
         raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {tuple(shape)} of {dtypes[0]}, got {tuple(t.shape)} of {t.dtype}")
 
 
@@ -335,8 +353,8 @@ class DecodeLayer:
                  Ws: Optional[ExpertWeights] = None, Is: int = 0, eps: float = 1e-6, router_scale: float = 1.0,
                  out_scale: float = 1.0, score: str = "sigmoid", norm_topk: bool = True,
                  max_tokens: int = abi.MOE_DECODE_MAX_T):
-        if W.w2.dim() != 3:
-            raise ValueError("w2: expected (E, H, ...)")
+        if W.w2.dim() != 3 or not W.w2.is_cuda:
+            raise ValueError("w2: expected (E, H, ...) on a CUDA device")
         self.device = dev = W.w2.device
         self.H, self.E, self.k, self.I = W.w2.shape[1], E, k, I
         if (Ws is None) != (Is == 0):
@@ -348,40 +366,63 @@ class DecodeLayer:
             _check_weights("Ws", Ws, 1, Is, self.H, dev)
         self._keep = (W, Ws, w_router, expert_bias)
         self.max_tokens = max_tokens
-        with torch.cuda.device(dev):
-            n = moe_decode_workspace_bytes(abi.moe_dims(max_tokens, self.H, E, k, I), Is)
+        d = abi.moe_dims(max_tokens, self.H, E, k, I)
+        n = moe_decode_workspace_bytes(d, Is)
         if n == 0:
             raise ValueError(f"sizes of the layer: {moe_last_error()}")
         self.ws = torch.zeros(n, dtype=torch.uint8, device=dev)   # the first 256 bytes start at zero
         self._layer = abi.moe_layer(_ptr(w_router), _ptr(expert_bias), W.c_struct(),
                                     Ws.c_struct() if Ws is not None else abi.moe_experts_w(), Is, eps, router_scale,
                                     out_scale, router_cfg(score, norm_topk))
+        self._plans = {}
+        self._run = load().moe_decode_run
+        self._plan(max_tokens)
+
+    def _plan(self, T: int):
+        """The prepared call for T tokens: (plan, reference to it, templates of the outputs)."""
+        plan = abi.moe_decode_plan()
+        d = abi.moe_dims(T, self.H, self.E, self.k, self.I)
+        with torch.cuda.device(self.device):
+            check(load().moe_decode_prepare(ctypes.byref(self._layer), ctypes.byref(d), ctypes.byref(plan)), "moe_decode")
+            idx = torch.empty((T, self.k), dtype=torch.int32, device=self.device)
+        self._plans[T] = (plan, ctypes.byref(plan), idx, idx.view(torch.float32))
+        return self._plans[T]
 
     def __call__(self, x, *, residual=None, logits=None, y=None, topk_idx=None, topk_w=None, stream=None):
-        dev, k = self.device, self.k
-        T = x.shape[0]
+        dev, T = self.device, x.shape[0]
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens, but the layer was made for max_tokens = {self.max_tokens}")
         _want("x", x, (T, self.H), (torch.bfloat16,), dev)
-        _want("residual", residual, (T, self.H), (torch.bfloat16,), dev)
-        _want("logits", logits, (T, self.E), (torch.float32,), dev)
-        _want("y", y, (T, self.H), (torch.bfloat16,), dev)
-        _want("topk_idx", topk_idx, (T, k), (torch.int32,), dev)
-        _want("topk_w", topk_w, (T, k), (torch.float32,), dev)
-        y = torch.empty_like(x) if y is None else y
-        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_idx is None else topk_idx
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
-        d = abi.moe_dims(T, self.H, self.E, k, self.I)
+        if residual is not None:
+            _want("residual", residual, (T, self.H), (torch.bfloat16,), dev)
+        if logits is not None:
+            _want("logits", logits, (T, self.E), (torch.float32,), dev)
+        _, plan, like_idx, like_w = self._plans.get(T) or self._plan(T)
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _want("y", y, (T, self.H), (torch.bfloat16,), dev)
+        if topk_idx is None:
+            topk_idx = torch.empty_like(like_idx)
+        else:
+            _want("topk_idx", topk_idx, (T, self.k), (torch.int32,), dev)
+        if topk_w is None:
+            topk_w = torch.empty_like(like_w)
+        else:
+            _want("topk_w", topk_w, (T, self.k), (torch.float32,), dev)
         if torch.cuda.current_device() != dev.index:
             with torch.cuda.device(dev):
-                return self._run(d, x, logits, residual, topk_idx, topk_w, y, stream)
-        return self._run(d, x, logits, residual, topk_idx, topk_w, y, stream)
-
-    def _run(self, d, x, logits, residual, topk_idx, topk_w, y, stream):
-        check(load().moe_decode(ctypes.byref(self._layer), ctypes.byref(d), x.data_ptr(), _ptr(logits), _ptr(residual),
-                                topk_idx.data_ptr(), topk_w.data_ptr(), y.data_ptr(), self.ws.data_ptr(),
-                                self.ws.numel(), _stream(stream)), "moe_decode")
+                st = self._go(plan, x, logits, residual, topk_idx, topk_w, y, stream)
+        else:
+            st = self._go(plan, x, logits, residual, topk_idx, topk_w, y, stream)
+        if st:
+            check(st, "moe_decode")
         return y, topk_idx, topk_w
+
+    def _go(self, plan, x, logits, residual, topk_idx, topk_w, y, stream):
+        return self._run(plan, x.data_ptr(), None if logits is None else logits.data_ptr(),
+                         None if residual is None else residual.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(),
+                         y.data_ptr(), self.ws.data_ptr(), self.ws.numel(), _stream_on(stream, self.device.index))
 
 
 def moe_profile_hook(ev_begin, ev_end, stage: int) -> None:

@@ -32,6 +32,7 @@
 // Bound: HBM for bf16 experts from a few tokens on; latency (barriers, first
 // loads, launch) at one token.
 #include <algorithm>
+#include <cstring>
 
 #include "common.cuh"
 #include "internal.h"
@@ -784,8 +785,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
     }
 }
 
+// What moe_decode_prepare leaves in the caller's moe_decode_plan.
+struct Plan {
+    DecodeArgs a;
+    uint64_t magic;
+    size_t smem, ws_bytes, ws_lg, ws_h, ws_hs;
+    int device, grid;
+    cudaError_t (*launch)(const Plan&, const DecodeArgs&, cudaStream_t);
+};
+constexpr uint64_t kPlanMagic = 0x6d6f65646563ull;
+static_assert(sizeof(Plan) + alignof(Plan) <= sizeof(moe_decode_plan), "moe_decode_plan holds a Plan at any address");
+
 template <int FMT, int NT, bool DUAL>
-cudaError_t run(DecodeArgs& a, cudaStream_t s) {
+cudaError_t launch(const Plan& p, const DecodeArgs& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_decode<FMT, NT, DUAL>, a);
+}
+
+template <int FMT, int NT, bool DUAL>
+cudaError_t plan(Plan& p) {
+    DecodeArgs& a = p.a;
     const DeviceInfo& di = device_info();
     using F = Fmt<FMT>;
     // + 1 KB: the ring starts on a multiple of that
@@ -820,36 +848,26 @@ cudaError_t run(DecodeArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // parts of the router's rows: work for all CTAs, at most 8 to sum
     a.parts = std::max(1, std::min(8, di.sm_count / a.E));
-    auto kern = k_decode<FMT, NT, DUAL>;
-    if ((e = ensure_smem(kern, smem)) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(di.sm_count);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    p.smem = smem;
+    p.grid = di.sm_count;
+    p.launch = launch<FMT, NT, DUAL>;
+    return ensure_smem(k_decode<FMT, NT, DUAL>, smem);
 }
 
 template <int FMT>
-cudaError_t run_fmt(DecodeArgs& a, bool dual, cudaStream_t s) {
-    if (a.T <= 8) return dual ? run<FMT, 1, true>(a, s) : run<FMT, 1, false>(a, s);
-    return dual ? run<FMT, 2, true>(a, s) : run<FMT, 2, false>(a, s);
+cudaError_t plan_fmt(Plan& p, bool dual) {
+    if (p.a.T <= 8) return dual ? plan<FMT, 1, true>(p) : plan<FMT, 1, false>(p);
+    return dual ? plan<FMT, 2, true>(p) : plan<FMT, 2, false>(p);
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct DecodeWs {
-    size_t sync, lg, h, hs, total;
+    size_t lg, h, hs, total;                    // behind 256 bytes of barrier count
 };
 
 DecodeWs ws_layout(const moe_dims* d, int Is) {
     DecodeWs L{};
-    L.sync = 0;
     size_t off = 256;
     L.lg = off;
     off = align256(off + (size_t)8 * d->T * d->E * 8);
@@ -890,6 +908,42 @@ WMat mat(const void* w, const void* scale, const void* bias, const float* glob, 
 
 bool misaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
+// The layer and the sizes, on the host.
+moe_status check_layer(const moe_layer* L, const moe_dims* d) {
+    if (!L) return refuse(MOE_ERR_NULL, "layer is NULL");
+    moe_status st = check_sizes(d, L->Is);
+    if (st != MOE_OK) return st;
+    if (L->router.score != MOE_SCORE_SIGMOID && L->router.score != MOE_SCORE_SOFTMAX)
+        return refuse(MOE_ERR_UNSUPPORTED, "router score");
+    if (L->router.norm_topk != 0 && L->router.norm_topk != 1) return refuse(MOE_ERR_UNSUPPORTED, "norm_topk");
+    if (misaligned(L->w_router, 16)) return refuse(MOE_ERR_ALIGN, "w_router not 16-byte aligned");
+    if (misaligned(L->expert_bias, 4)) return refuse(MOE_ERR_ALIGN, "expert_bias not 4-byte aligned");
+    if ((st = validate_weights(&L->W)) != MOE_OK) return st;
+    if (L->Is > 0) {
+        if ((st = validate_weights(&L->Ws)) != MOE_OK) return st;
+        if (L->Ws.fmt != L->W.fmt || L->Ws.act != L->W.act)
+            return refuse(MOE_ERR_UNSUPPORTED, "the shared expert's format or activation differs from the routed experts'");
+    }
+    return MOE_OK;
+}
+
+// What a call brings.
+moe_status check_call(const void* x, const float* logits, const float* w_router, const void* residual,
+                      const int32_t* topk_idx, const float* topk_w, const void* y, const void* ws, size_t ws_bytes,
+                      size_t need) {
+    if (!x || !y) return refuse(MOE_ERR_NULL, "x or y is NULL");
+    if (!topk_idx || !topk_w) return refuse(MOE_ERR_NULL, "topk_idx or topk_w is NULL");
+    if (!logits && !w_router) return refuse(MOE_ERR_NULL, "w_router is NULL (routing from x)");
+    if (misaligned(x, 16) || misaligned(y, 16)) return refuse(MOE_ERR_ALIGN, "x or y not 16-byte aligned");
+    if (misaligned(residual, 16)) return refuse(MOE_ERR_ALIGN, "residual not 16-byte aligned");
+    if (misaligned(logits, 4) || misaligned(topk_idx, 4) || misaligned(topk_w, 4))
+        return refuse(MOE_ERR_ALIGN, "logits, topk_idx or topk_w not 4-byte aligned");
+    if (!ws) return refuse(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if (misaligned(ws, 256)) return refuse(MOE_ERR_ALIGN, "workspace not 256-byte aligned");
+    if (ws_bytes < need) return refuse(MOE_ERR_WORKSPACE, "workspace smaller than moe_decode_workspace_bytes()");
+    return MOE_OK;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -901,42 +955,16 @@ size_t moe_decode_workspace_bytes(const moe_dims* d, int32_t Is) {
     return check_sizes(d, Is) == MOE_OK ? ws_layout(d, Is).total : 0;
 }
 
-moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void* x, const float* logits,
-                      const void* residual, int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes,
-                      moe_stream_t stream) {
-    if (!L) return refuse(MOE_ERR_NULL, "layer is NULL");
-    moe_status st = check_sizes(d, L->Is);
+moe_status moe_decode_prepare(const moe_layer* L, const moe_dims* d, moe_decode_plan* out) {
+    const moe_status st = check_layer(L, d);
     if (st != MOE_OK) return st;
-    if (L->router.score != MOE_SCORE_SIGMOID && L->router.score != MOE_SCORE_SOFTMAX)
-        return refuse(MOE_ERR_UNSUPPORTED, "router score");
-    if (L->router.norm_topk != 0 && L->router.norm_topk != 1) return refuse(MOE_ERR_UNSUPPORTED, "norm_topk");
-    if (d->T == 0) return set_last_launch_count(0), MOE_OK;   // empty batch: nothing to do
-    if (!x || !y) return refuse(MOE_ERR_NULL, "x or y is NULL");
-    if (!topk_idx || !topk_w) return refuse(MOE_ERR_NULL, "topk_idx or topk_w is NULL");
-    if (!logits && !L->w_router) return refuse(MOE_ERR_NULL, "w_router is NULL (routing from x)");
-    if (misaligned(x, 16) || misaligned(y, 16)) return refuse(MOE_ERR_ALIGN, "x or y not 16-byte aligned");
-    if (misaligned(residual, 16)) return refuse(MOE_ERR_ALIGN, "residual not 16-byte aligned");
-    if (!logits && misaligned(L->w_router, 16)) return refuse(MOE_ERR_ALIGN, "w_router not 16-byte aligned");
-    if (misaligned(logits, 4) || misaligned(L->expert_bias, 4) || misaligned(topk_idx, 4) || misaligned(topk_w, 4))
-        return refuse(MOE_ERR_ALIGN, "logits, expert_bias, topk_idx or topk_w not 4-byte aligned");
-    if ((st = validate_weights(&L->W)) != MOE_OK) return st;
-    if (L->Is > 0) {
-        if ((st = validate_weights(&L->Ws)) != MOE_OK) return st;
-        if (L->Ws.fmt != L->W.fmt || L->Ws.act != L->W.act)
-            return refuse(MOE_ERR_UNSUPPORTED, "the shared expert's format or activation differs from the routed experts'");
-    }
+    if (!out) return refuse(MOE_ERR_NULL, "plan is NULL");
     const DecodeWs wl = ws_layout(d, L->Is);
-    if (!ws) return refuse(MOE_ERR_WORKSPACE, "workspace is NULL");
-    if (misaligned(ws, 256)) return refuse(MOE_ERR_ALIGN, "workspace not 256-byte aligned");
-    if (ws_bytes < wl.total) return refuse(MOE_ERR_WORKSPACE, "workspace smaller than moe_decode_workspace_bytes()");
-    char* b = static_cast<char*>(ws);
     const bool dual = L->W.act == MOE_ACT_SWIGLU;
-    DecodeArgs a{};
-    a.x = static_cast<const uint16_t*>(x);
-    a.logits = logits;
+    Plan p{};
+    DecodeArgs& a = p.a;
     a.w_router = L->w_router;
     a.ebias = L->expert_bias;
-    a.residual = static_cast<const uint16_t*>(residual);
     a.W1 = mat(L->W.w1, L->W.w1_scale, L->W.w1_bias, L->W.w1_global, dual ? 2 * d->I : d->I, d->H);
     a.W2 = mat(L->W.w2, L->W.w2_scale, L->W.w2_bias, L->W.w2_global, d->H, d->I);
     if (L->Is > 0) {
@@ -956,26 +984,67 @@ moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void* x, cons
     a.limit = L->W.swiglu_limit;
     a.softmax = L->router.score == MOE_SCORE_SOFTMAX;
     a.no_norm = L->router.norm_topk == 0;
-    a.idx = topk_idx;
-    a.w = topk_w;
-    a.y = static_cast<uint16_t*>(y);
-    a.sync = reinterpret_cast<unsigned long long*>(b + wl.sync);
-    a.lg = reinterpret_cast<double*>(b + wl.lg);
-    a.h = reinterpret_cast<uint16_t*>(b + wl.h);
-    a.hs = reinterpret_cast<uint16_t*>(b + wl.hs);
     a.wait_limit = sm100::kWaitLimit;
     a.err = device_info().err_word;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = L->W.fmt == MOE_W_BF16          ? run_fmt<kBf16>(a, dual, s)
-                          : L->W.fmt == MOE_W_AFFINE4_G64 ? run_fmt<kAffine>(a, dual, s)
-                                                          : run_fmt<kNvfp4>(a, dual, s);
-    if (e == cudaErrorNotSupported) return refuse(MOE_ERR_UNSUPPORTED, "moe_decode: shared memory of this device");
-    if (e != cudaSuccess) {
-        set_last_error(cudaGetErrorString(e));
-        return MOE_ERR_CUDA;
-    }
+    p.ws_bytes = wl.total;
+    p.ws_lg = wl.lg;
+    p.ws_h = wl.h;
+    p.ws_hs = wl.hs;
+    p.magic = kPlanMagic;
+    cudaError_t e = cudaGetDevice(&p.device);
+    if (e == cudaSuccess && d->T > 0)            // an empty batch launches nothing
+        e = L->W.fmt == MOE_W_BF16          ? plan_fmt<kBf16>(p, dual)
+            : L->W.fmt == MOE_W_AFFINE4_G64 ? plan_fmt<kAffine>(p, dual)
+                                            : plan_fmt<kNvfp4>(p, dual);
+    if (e == cudaErrorNotSupported) return refuse(MOE_ERR_UNSUPPORTED, "moe_decode: shared memory or driver of this device");
+    if (e != cudaSuccess) return refuse(MOE_ERR_CUDA, cudaGetErrorString(e));
+    memset(out, 0, sizeof *out);
+    memcpy(out, &p, sizeof p);
+    return MOE_OK;
+}
+
+moe_status moe_decode_run(const moe_decode_plan* plan, const void* x, const float* logits, const void* residual,
+                          int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    if (!plan) return refuse(MOE_ERR_NULL, "plan is NULL");
+    Plan p;
+    memcpy(&p, plan, sizeof p);
+    if (p.magic != kPlanMagic) return refuse(MOE_ERR_UNSUPPORTED, "not a plan of moe_decode_prepare");
+    if (p.a.T == 0) return set_last_launch_count(0), MOE_OK;   // empty batch: nothing to do
+    const moe_status st = check_call(x, logits, p.a.w_router, residual, topk_idx, topk_w, y, ws, ws_bytes, p.ws_bytes);
+    if (st != MOE_OK) return st;
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev != p.device)
+        return refuse(MOE_ERR_UNSUPPORTED, "the plan was prepared for another device");
+    char* b = static_cast<char*>(ws);
+    p.a.x = static_cast<const uint16_t*>(x);
+    p.a.logits = logits;
+    p.a.residual = static_cast<const uint16_t*>(residual);
+    p.a.idx = topk_idx;
+    p.a.w = topk_w;
+    p.a.y = static_cast<uint16_t*>(y);
+    p.a.sync = reinterpret_cast<unsigned long long*>(b);
+    p.a.lg = reinterpret_cast<double*>(b + p.ws_lg);
+    p.a.h = reinterpret_cast<uint16_t*>(b + p.ws_h);
+    p.a.hs = reinterpret_cast<uint16_t*>(b + p.ws_hs);
+    if (e == cudaSuccess) e = p.launch(p, p.a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return refuse(MOE_ERR_CUDA, cudaGetErrorString(e));
     set_last_launch_count(1);
     return MOE_OK;
+}
+
+moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void* x, const float* logits,
+                      const void* residual, int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes,
+                      moe_stream_t stream) {
+    moe_status st = check_layer(L, d);
+    if (st != MOE_OK) return st;
+    if (d->T == 0) return set_last_launch_count(0), MOE_OK;   // empty batch: nothing to do
+    st = check_call(x, logits, L->w_router, residual, topk_idx, topk_w, y, ws, ws_bytes, ws_layout(d, L->Is).total);
+    if (st != MOE_OK) return st;
+    moe_decode_plan plan;
+    st = moe_decode_prepare(L, d, &plan);
+    return st != MOE_OK ? st
+                        : moe_decode_run(&plan, x, logits, residual, topk_idx, topk_w, y, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

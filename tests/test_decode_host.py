@@ -82,6 +82,16 @@ def test_layer(lib, layer, status):
     assert _call(lib, _layer(**layer)) == status
 
 
+def test_prepared_plan(lib):
+    """What prepare refuses, run never sees; run refuses anything that is no plan."""
+    plan = abi.moe_decode_plan()
+    assert lib.moe_decode_prepare(ctypes.byref(_layer()), ctypes.byref(_d(T=17)), ctypes.byref(plan)) == abi.MOE_ERR_SHAPE
+    assert lib.moe_decode_prepare(ctypes.byref(_layer()), ctypes.byref(_d()), None) == abi.MOE_ERR_NULL
+    args = (0x10000, None, None, 0x20000, 0x30000, 0x40000, 0x1000000, 1 << 24, None)
+    assert lib.moe_decode_run(None, *args) == abi.MOE_ERR_NULL
+    assert lib.moe_decode_run(ctypes.byref(plan), *args) == abi.MOE_ERR_UNSUPPORTED
+
+
 def test_null_layer_and_empty_batch(lib):
     assert lib.moe_decode(None, ctypes.byref(_d()), 0x10000, None, None, 0x20000, 0x30000, 0x40000, 0x1000000, 1 << 24,
                           None) == abi.MOE_ERR_NULL
