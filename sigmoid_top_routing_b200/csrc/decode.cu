@@ -26,8 +26,8 @@
 // stream of weights for long: the producer fetches the shared expert's rows
 // before the routing is known and the down rows before h is.
 //
-// Router sums and scores are 64-bit: E * H * T is small here, and picks are
-// then those of the real-number scores up to ties.
+// Router sums carry ~46 bits (fp32 pairs) and close scores are compared in 64: E * H * T
+// is small here, and picks are then those of the real-number scores up to ties.
 //
 // Bound: HBM for bf16 experts from a few tokens on; latency (barriers, first
 // loads, launch) at one token.
@@ -53,7 +53,7 @@ constexpr int kThreads = kCThreads + kGroups * 32;   // + a producer warp per gr
 constexpr int kMaxE = 257;                      // 256 experts and the shared one
 constexpr int kMaxK = 32;
 constexpr int kMaxStages = 16;
-constexpr int kMaxParts = 8;                    // parts of a router row
+constexpr int kMaxParts = 4;                    // parts of a router row
 
 struct WMat {                                   // one weight tensor of the experts
     CUtensorMap map;                            // (experts * rows) rows of codes
@@ -79,7 +79,7 @@ struct DecodeArgs {
     float* w;
     uint16_t* y;
     unsigned long long* sync;                   // barrier arrivals: a multiple of the grid size between calls
-    double* lg;                                 // (parts, T, E): logits, each part over H / parts of the row
+    float2* lg;                                 // (parts, T, E): logits (hi, lo), each part over H / parts of the row
     int parts;
     uint16_t* h;                                // (T k, I)
     uint16_t* hs;                               // (T, Is)
@@ -126,16 +126,44 @@ MOE_DEV float unkey32(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7ff
 
 MOE_DEV double sigmoid64(double L) { return 1.0 / (1.0 + exp(-L)); }
 
+// Unevaluated fp32 sums hi + lo (about 46 bits), for the router's dot products:
+// double-precision arithmetic runs at a small fraction of the fp32 rate.
+struct F2 {
+    float hi, lo;
+};
+MOE_DEV void add_to(F2& a, float v) {           // a += v, error-free in hi
+    const float s = a.hi + v, t = s - a.hi;
+    a.lo += (a.hi - (s - t)) + (v - t);
+    a.hi = s;
+}
+MOE_DEV void add_to(F2& a, F2 b) {
+    add_to(a, b.hi);
+    a.lo += b.lo;
+}
+MOE_DEV void fma_to(F2& a, float x, float y) {  // a += x y, the product's rounding error kept
+    const float p = x * y;
+    const float e = fmaf(x, y, -p);
+    add_to(a, p);
+    a.lo += e;
+}
+// An infinite or NaN sum is hi alone (its error terms are NaN).
+MOE_DEV double f2_value(F2 a) { return fabsf(a.hi) <= 3.402823466e38f ? (double)a.hi + (double)a.lo : (double)a.hi; }
+
 // The logit of (token t, expert e): given, or the parts' sum in order.
-MOE_DEV double logit_of(const DecodeArgs& a, int t, int e) {
-    if (a.logits) return (double)__ldg(a.logits + (size_t)t * a.E + e);
-    double v[kMaxParts], sum = 0.0;
+MOE_DEV F2 logit_f2(const DecodeArgs& a, int t, int e) {
+    if (a.logits) return F2{__ldg(a.logits + (size_t)t * a.E + e), 0.0f};
+    float2 v[kMaxParts];
 #pragma unroll
-    for (int p = 0; p < kMaxParts; ++p) v[p] = p < a.parts ? __ldcg(a.lg + ((size_t)p * a.T + t) * a.E + e) : 0.0;
+    for (int p = 0; p < kMaxParts; ++p)
+        if (p < a.parts) v[p] = __ldcg(a.lg + ((size_t)p * a.T + t) * a.E + e);
+    F2 sum{v[0].x, v[0].y};
 #pragma unroll
-    for (int p = 0; p < kMaxParts; ++p) sum += v[p];
+    for (int p = 1; p < kMaxParts; ++p)
+        if (p < a.parts) add_to(sum, F2{v[p].x, v[p].y});
     return sum;
 }
+MOE_DEV double logit_of(const DecodeArgs& a, int t, int e) { return f2_value(logit_f2(a, t, e)); }
+
 // Softmax statistics of a token's logits, by one warp: max and sum of exp
 // (NaN when a logit is NaN, which makes every score of the row NaN).
 MOE_DEV void softmax_stats64(const DecodeArgs& a, int t, double& m, double& z) {
@@ -364,6 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         *s_abort = 0;
         fence_mbar_init();
     }
+    if (warp == kCw && lane < (a.Is > 0 ? 4 : 2))
+        tma_prefetch_desc(lane == 0 ? &a.W1.map : lane == 1 ? &a.W2.map : lane == 2 ? &a.S1.map : &a.S2.map);
     __syncthreads();
 
     const int grp = warp < kCw ? warp / kGw : warp - kCw;
@@ -508,6 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
             for (int c = c0; c < c1 && ahead < Sg && ok; ++c, ++ahead) weights(a.sd2, m, u, false, c);
             return ahead < Sg && ok;
         });
+        // the weights of the picks are first needed by the down products
+        for (int t = grp; t < a.T; t += kGroups)
+            weigh_token(a, t, s_pick + t * kMaxK, s_wt + t * kMaxK, cta == 0);
         named_bar(6, kThreads);                 // every h is written
         fence_proxy_async_all();
         if (*s_abort) ok = false;
@@ -541,15 +574,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         // Grid barrier: arrivals only ever add up, gridDim.x per barrier, so what
         // is there when a CTA looks, rounded down to a multiple of that, is where
         // the count stood before its next own arrival.
-        unsigned long long target = 0;
-        if (tid == 0) {
-            asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(target) : "l"(a.sync) : "memory");
-            target -= target % (uint32_t)G;
-        }
-        auto arrive = [&]() {                   // thread 0, after a barrier of all consumers
-            target += (uint32_t)G;
-            __threadfence();
+        unsigned long long seen = 0, target = 0;
+        if (tid == 0) asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(seen) : "l"(a.sync) : "memory");
+        // thread 0: the release covers what it and, through the CTA's barrier just
+        // before, the other consumers wrote
+        auto arrive = [&]() {
             asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(a.sync), "l"(1ull) : "memory");
+            target = (target ? target : seen - seen % (uint32_t)G) + (uint32_t)G;
         };
         auto grid_wait = [&]() {                // thread 0
             bool ok = false;
@@ -566,34 +597,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         // ---- router: work item (expert, part of H); a warp takes one token's
         // row, or a share of it when there are fewer tokens than warps
         if (!a.logits) {
-            double* s_d = reinterpret_cast<double*>(s_red);      // [kCw]
+            F2* s_d = reinterpret_cast<F2*>(s_red);              // [kCw]
             const int wpt = a.T > 8 ? 1 : a.T > 4 ? 2 : a.T > 2 ? 4 : a.T > 1 ? 8 : 16;   // warps per token
             const int t = warp / wpt, ws = warp - t * wpt;
             const int nq = a.H / 4;                              // groups of 4 k
             for (int it = cta; it < a.E * a.parts; it += G) {
                 const int e = it / a.parts, p = it - e * a.parts;
                 const int q1 = part(nq, p + 1, a.parts);
-                double acc = 0.0;
+                F2 acc{0.0f, 0.0f}, acc2{0.0f, 0.0f};
                 if (t < a.T)
 #pragma unroll 4
                     for (int q = part(nq, p, a.parts) + ws * 32 + lane; q < q1; q += wpt * 32) {
                         const float4 w = __ldg(reinterpret_cast<const float4*>(a.w_router + (size_t)e * a.H) + q);
                         const uint2 v = *(reinterpret_cast<const uint2*>(a.x + (size_t)t * a.H) + q);
-                        acc = fma((double)w.x, (double)bf16lo(v.x), acc);
-                        acc = fma((double)w.y, (double)bf16hi(v.x), acc);
-                        acc = fma((double)w.z, (double)bf16lo(v.y), acc);
-                        acc = fma((double)w.w, (double)bf16hi(v.y), acc);
+                        fma_to(acc, w.x, bf16lo(v.x));
+                        fma_to(acc2, w.y, bf16hi(v.x));
+                        fma_to(acc, w.z, bf16lo(v.y));
+                        fma_to(acc2, w.w, bf16hi(v.y));
                     }
-                for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+                add_to(acc, acc2);
+                for (int o = 16; o > 0; o >>= 1)
+                    add_to(acc, F2{__shfl_xor_sync(0xffffffffu, acc.hi, o), __shfl_xor_sync(0xffffffffu, acc.lo, o)});
                 if (lane == 0) s_d[warp] = acc;
                 named_bar(5, kCThreads);
-                if (tid < a.T) {
-                    double v = 0.0;
-                    for (int w = 0; w < wpt; ++w) v += s_d[tid * wpt + w];
-                    __stcg(a.lg + ((size_t)p * a.T + tid) * a.E + e, v);
+                if (warp == 0) {                                 // the warps of a token, by shuffles among 16 lanes
+                    acc = s_d[lane & 15];
+                    for (int o = wpt >> 1; o > 0; o >>= 1)
+                        add_to(acc, F2{__shfl_xor_sync(0xffffffffu, acc.hi, o), __shfl_xor_sync(0xffffffffu, acc.lo, o)});
+                    const int tt = lane / wpt;
+                    if (lane < 16 && tt * wpt == lane && tt < a.T)
+                        __stcg(a.lg + ((size_t)p * a.T + tt) * a.E + e, make_float2(acc.hi, acc.lo));
                 }
-                named_bar(5, kCThreads);
+                if (it + G < a.E * a.parts) named_bar(5, kCThreads);
             }
+            __syncwarp();
             if (tid == 0) arrive();
         }
         // ---- token rows into shared memory (while the other CTAs' logits arrive)
@@ -611,7 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         uint32_t* s_key = reinterpret_cast<uint32_t*>(s_red);          // [T][E]
         for (int i = tid; i < a.T * a.E; i += kCThreads) {
             const int t = i / a.E, e = i - t * a.E;
-            const float L = (float)logit_of(a, t, e);
+            const F2 l2 = logit_f2(a, t, e);
+            const float L = fabsf(l2.hi) <= 3.402823466e38f ? l2.hi + l2.lo : l2.hi;
             s_key[i] = a.softmax ? __float_as_uint(L)
                                  : key32(1.0f / (1.0f + expf(-L)) + (a.ebias ? __ldg(a.ebias + e) : 0.0f));
         }
@@ -650,15 +688,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 fence_proxy_async_all();        // (the down stages read it through the async proxy)
                 named_bar(5, kCThreads);
                 if (tid == 0) arrive();
-                // the weights of the picks are first needed below: they fill the wait
-                if (warp < a.T) weigh_token(a, warp, s_pick + warp * kMaxK, s_wt + warp * kMaxK, cta == 0);
                 if (tid == 0) grid_wait();
                 named_bar(6, kThreads);
                 if (*s_abort) dead = true;
             }
+            float res = 0.0f;                   // this thread's element of the tile's residual
             if (!up) {
                 for (int i = lane; i < kRows * TT; i += 32) yw[i] = ysw[i] = 0.0f;
                 __syncwarp();
+                int r0, nr;
+                rows_of_tile(phase - 2, r0, nr);
+                const int r = tid % kRows, t = tid / kRows;
+                if (a.residual && r < nr && t < a.T) res = bf16f(a.residual[(size_t)t * a.H + r0 + r]);
             }
             walk(phase, nact, [&](const Unit& u, const WMat& m, int c0, int c1) {
                 const uint32_t mask = s_mask[u.e];
@@ -762,11 +803,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 int r0, nr;
                 rows_of_tile(phase - 2, r0, nr);
                 named_bar(5, kCThreads);
-                for (int i = tid; i < kRows * TT; i += kCThreads) {
-                    const int r = i % kRows, t = i / kRows;
-                    if (r >= nr || t >= a.T || dead) continue;
+                if (tid < kRows * TT) do {
+                    const int r = tid % kRows, t = tid / kRows;
+                    if (r >= nr || t >= a.T || dead) break;
                     const size_t o = (size_t)t * a.H + r0 + r;
-                    const float res = a.residual ? bf16f(a.residual[o]) : 0.0f;
                     float v = 0.0f;
 #pragma unroll
                     for (int w = 0; w < kCw; ++w) v += s_red[(w * kRows + r) * TT + t];
@@ -778,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                     }
                     if (a.residual) v += res;
                     a.y[o] = f2bf16(v);
-                }
+                } while (0);
                 named_bar(5, kCThreads);
             }
         }
@@ -846,8 +886,8 @@ cudaError_t plan(Plan& p) {
     if (e == cudaSuccess && a.Is > 0) e = map(a.S1, a.S1.rows, c1);
     if (e == cudaSuccess && a.Is > 0) e = map(a.S2, a.S2.rows, c2);
     if (e != cudaSuccess) return e;
-    // parts of the router's rows: work for all CTAs, at most 8 to sum
-    a.parts = std::max(1, std::min(8, di.sm_count / a.E));
+    // parts of the router's rows: work for all CTAs
+    a.parts = std::max(1, std::min(kMaxParts, di.sm_count / a.E));
     p.smem = smem;
     p.grid = di.sm_count;
     p.launch = launch<FMT, NT, DUAL>;
@@ -870,7 +910,7 @@ DecodeWs ws_layout(const moe_dims* d, int Is) {
     DecodeWs L{};
     size_t off = 256;
     L.lg = off;
-    off = align256(off + (size_t)8 * d->T * d->E * 8);
+    off = align256(off + (size_t)kMaxParts * d->T * d->E * 8);
     L.h = off;
     off = align256(off + (size_t)d->T * d->k * d->I * 2);
     L.hs = off;
@@ -1024,7 +1064,7 @@ moe_status moe_decode_run(const moe_decode_plan* plan, const void* x, const floa
     p.a.w = topk_w;
     p.a.y = static_cast<uint16_t*>(y);
     p.a.sync = reinterpret_cast<unsigned long long*>(b);
-    p.a.lg = reinterpret_cast<double*>(b + p.ws_lg);
+    p.a.lg = reinterpret_cast<float2*>(b + p.ws_lg);
     p.a.h = reinterpret_cast<uint16_t*>(b + p.ws_h);
     p.a.hs = reinterpret_cast<uint16_t*>(b + p.ws_hs);
     if (e == cudaSuccess) e = p.launch(p, p.a, reinterpret_cast<cudaStream_t>(stream));
