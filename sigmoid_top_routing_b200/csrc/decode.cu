@@ -53,6 +53,7 @@ constexpr int kThreads = kCThreads + kGroups * 32;   // + a producer warp per gr
 constexpr int kMaxE = 257;                      // 256 experts and the shared one
 constexpr int kMaxK = 32;
 constexpr int kMaxStages = 16;
+constexpr int kMostCounted = 1 << 17;            // comparisons of a selection by counting
 constexpr int kMaxParts = 4;                    // parts of a router row
 
 struct WMat {                                   // one weight tensor of the experts
@@ -64,6 +65,15 @@ struct WMat {                                   // one weight tensor of the expe
     const float* glob;
     int rows, K;                                // rows per expert, row length
 };
+
+// Division by a number the host knows: a runtime divide costs ~150 cycles of
+// latency, and a one-token call has a dozen in a row.  m = floor(2^64 / n) + 1
+// gives floor(v m / 2^64) = floor(v / n) for v, n < 2^32; m = 0 stands for n = 1.
+struct Divisor {
+    uint64_t m;
+};
+Divisor divisor(uint32_t n) { return Divisor{n == 1 ? 0 : ~0ull / n + 1}; }
+MOE_DEV uint32_t div_by(uint32_t v, Divisor d) { return d.m ? (uint32_t)__umul64hi(v, d.m) : v; }
 
 struct DecodeArgs {
     const uint16_t* x;
@@ -80,7 +90,9 @@ struct DecodeArgs {
     uint16_t* y;
     unsigned long long* sync;                   // barrier arrivals: a multiple of the grid size between calls
     float2* lg;                                 // (parts, T, E): logits (hi, lo), each part over H / parts of the row
-    int parts;
+    int parts;                                  // 1, 2 or 4
+    int up_stages, i_stages, is_stages;         // stages of a row: H; I and Is in the down products
+    Divisor by_grid, by_groups, by_I, by_E, by_i_stages;
     uint16_t* h;                                // (T k, I)
     uint16_t* hs;                               // (T, Is)
     int stages;                                 // ring slots per group
@@ -94,7 +106,7 @@ template <int NT>
 struct Layout {                                 // shared memory (byte offsets)
     static constexpr int kTok = 8 * NT;
     static constexpr int kMask = 0;                                   // kMaxE words: tokens of an expert
-    static constexpr int kList = kMask + 1040;                        // active expert ids
+    static constexpr int kList = kMask + (kMaxE + kTok * (kMaxK + 1) + 3) / 4 * 16;   // (behind the masks: keys by rank) active expert ids
     static constexpr int kPick = kList + 1040;                        // [kTok][kMaxK] expert of a pick
     static constexpr int kWt = kPick + kTok * kMaxK * 4;              // [kTok][kMaxK] routing weight
     static constexpr int kSlot = kWt + kTok * kMaxK * 4;              // [kTok][256] bytes: pick number of an expert
@@ -179,47 +191,60 @@ MOE_DEV double score64(const DecodeArgs& a, double L, double m, double z) {
     return a.softmax ? (z == z ? exp(L - m) / z : z) : sigmoid64(L);
 }
 
-// Picks of one token by one warp.  s_key[e] holds fp32 score keys (sigmoid) or
-// logits (softmax); lane sees experts lane + 32 i.  The fp32 scores are within
-// 2e-6 (1 + |c|) of the 64-bit ones, so where the first k + 1 of them are
-// further apart than twice that, their order is the 64-bit order; else the
-// token is ranked again from 64-bit scores.  This code runs once per launch, so it is kept short: straight-line code would cost more in
-// instruction fetches than it saves.
-MOE_DEV void select_token(const DecodeArgs& a, int t, uint32_t* s_key, int* pick, unsigned char* slot,
-                          uint32_t* mask) {
+// Turns a token's logits into score keys (softmax), by one warp.
+MOE_DEV void softmax_keys(const DecodeArgs& a, uint32_t* s_key) {
     const int lane = threadIdx.x & 31;
-    if (a.softmax) {
-        float m = -INFINITY, z = 0.0f;
-        for (int e = lane; e < a.E; e += 32) m = fmaxf(m, __uint_as_float(s_key[e]));
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        for (int e = lane; e < a.E; e += 32) z += expf(__uint_as_float(s_key[e]) - m);
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        for (int e = lane; e < a.E; e += 32) {
-            const float s = z == z ? expf(__uint_as_float(s_key[e]) - m) / z : z;
-            s_key[e] = key32(s + (a.ebias ? __ldg(a.ebias + e) : 0.0f));
-        }
-        __syncwarp();
+    float m = -INFINITY, z = 0.0f;
+    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, __uint_as_float(s_key[e]));
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int e = lane; e < a.E; e += 32) z += expf(__uint_as_float(s_key[e]) - m);
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    for (int e = lane; e < a.E; e += 32) {
+        const float s = z == z ? expf(__uint_as_float(s_key[e]) - m) / z : z;
+        s_key[e] = key32(s + (a.ebias ? __ldg(a.ebias + e) : 0.0f));
     }
+}
+
+// Picks of one token by one warp, from fp32 score keys: already ranked (counted)
+// or by k + 1 rounds of a warp-wide maximum.  The fp32 scores are within 2e-6
+// (1 + |c|) of the 64-bit ones, so where the first k + 1 of them are further
+// apart than twice that, their order is the 64-bit order; else the token is
+// ranked again from 64-bit scores.
+// (A round is ~500 cycles of latency, the count of a whole rank ~300 for 64
+// experts but E^2 T work: it is used up to kMostCounted comparisons.)
+MOE_DEV void select_token(const DecodeArgs& a, int t, bool counted, uint32_t* s_key, const uint32_t* s_sorted, int* pick,
+                          unsigned char* slot, uint32_t* mask) {
+    const int lane = threadIdx.x & 31;
     int my_e = 0;
     bool close = false;
-    uint32_t last = 0;
     const int rounds = min(a.k + 1, a.E);
-    for (int j = 0; j < rounds; ++j) {
-        uint32_t best = 0;
-        int be = 0xffff;
-        for (int e = lane; e < a.E; e += 32) {
-            const uint32_t c = s_key[e];
-            if (c > best) { best = c; be = e; }
+    if (counted) {
+        if (lane < a.k) my_e = pick[lane];
+        for (int j = lane; j + 1 < rounds; j += 32) {
+            const uint32_t hi = s_sorted[j], lo = s_sorted[j + 1];
+            const float c = unkey32(hi);
+            close |= hi > 1u && lo > 1u && !(c - unkey32(lo) > 4e-6f * (1.0f + fabsf(c)));   // both numbers
         }
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)be : 0xffffu);
-        if (lane == (e & 31)) s_key[e] = 0u;    // picked: below every NaN
-        if (lane == j) my_e = e;
-        if (j > 0 && last > 1u && top > 1u) {   // both numbers
-            const float c = unkey32(last);
-            close |= !(c - unkey32(top) > 4e-6f * (1.0f + fabsf(c)));
+        close = __any_sync(0xffffffffu, close);
+    } else {
+        uint32_t last = 0;
+        for (int j = 0; j < rounds; ++j) {
+            uint32_t best = 0;
+            int be = 0xffff;
+            for (int e = lane; e < a.E; e += 32) {
+                const uint32_t c = s_key[e];
+                if (c > best) { best = c; be = e; }
+            }
+            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+            const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)be : 0xffffu);
+            if (lane == (e & 31)) s_key[e] = 0u;    // picked: below every NaN
+            if (lane == j) my_e = e;
+            if (j > 0 && last > 1u && top > 1u) {
+                const float c = unkey32(last);
+                close |= !(c - unkey32(top) > 4e-6f * (1.0f + fabsf(c)));
+            }
+            last = top;
         }
-        last = top;
     }
     if (close) {                                // warp-uniform
         double m = 0.0, z = 1.0;
@@ -289,10 +314,9 @@ struct Unit {
     size_t row0, row1;                          // first weight row of either half of 8 rows
 };
 
-// Start of part i of n equal parts of v (v * (i + 1) must fit 32 bits).
-MOE_DEV int part(int v, int i, int n) { return (int)((uint32_t)v * (uint32_t)i / (uint32_t)n); }
-
-MOE_DEV int stages_of(int K, const StageDims& sd) { return (K + sd.k - 1) / sd.k; }
+// Start of part i of d.n equal parts of v (v * i below 2^32: at most 256 experts
+// of 16384 features times the groups of the grid, 592 on this part).
+MOE_DEV int part(int v, int i, Divisor d) { return (int)div_by((uint32_t)v * (uint32_t)i, d); }
 
 // Requests stage c of a unit's rows (and their scales).
 template <int FMT>
@@ -401,52 +425,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
 
     // Work of this group: equal parts, over all groups of the grid, of the
     // shared expert's features and of the routed experts' list (once it is known).
-    const int wk = cta * kGroups + grp, nwk = G * kGroups;
-    const int sf0 = part(a.Is, wk, nwk), sf1 = part(a.Is, wk + 1, nwk);
+    const int wk = cta * kGroups + grp;
     // This CTA's rows of y, in tiles of at most 16; each tile's list of
     // (expert, chunk of k) is dealt out to the groups in equal parts.
-    const int yr0 = part(a.H, cta, G), yr1 = part(a.H, cta + 1, G);
+    const int yr0 = part(a.H, cta, a.by_grid), yr1 = part(a.H, cta + 1, a.by_grid);
     const int ytiles = max(1, (yr1 - yr0 + kRows - 1) / kRows);
     // phases: 0 the shared expert's features, 1 the routed experts', 2.. tiles of y
     auto rows_of_tile = [&](int tile, int& r0, int& n) {
-        r0 = yr0 + part(yr1 - yr0, tile, ytiles);
-        n = yr0 + part(yr1 - yr0, tile + 1, ytiles) - r0;
+        const int rows = yr1 - yr0;
+        r0 = ytiles == 1 ? 0 : rows * tile / ytiles;
+        n = (ytiles == 1 ? rows : rows * (tile + 1) / ytiles) - r0;
+        r0 += yr0;
     };
     // Calls f(unit, weights, first chunk, end chunk) for the group's units of a
     // phase, in order; f returns false to stop.  A down unit is a run of chunks
     // of one expert: a tile's (expert, chunk) list is dealt out to the groups.
     auto walk = [&](int phase, int nact, auto&& f) {
         int p, end, li = 0, off = 0, r0 = 0, nr = 0;
-        const int i_chunks = stages_of(a.I, a.sd2), is_chunks = stages_of(a.Is, a.sd2);
         if (phase == 0) {
-            p = off = part(a.Is, wk, nwk);
-            end = part(a.Is, wk + 1, nwk);
+            p = off = part(a.Is, wk, a.by_groups);
+            end = part(a.Is, wk + 1, a.by_groups);
         } else if (phase == 1) {
-            p = part(nact * a.I, wk, nwk);
-            end = part(nact * a.I, wk + 1, nwk);
-            li = p / a.I;
+            p = part(nact * a.I, wk, a.by_groups);
+            end = part(nact * a.I, wk + 1, a.by_groups);
+            li = (int)div_by(p, a.by_I);
             off = p - li * a.I;
         } else {
             rows_of_tile(phase - 2, r0, nr);
             if (nr == 0) return;                // fewer rows than CTAs
-            const int total = nact * i_chunks + is_chunks;
-            p = part(total, grp, kGroups);
-            end = part(total, grp + 1, kGroups);
-            li = min(p / i_chunks, nact);
-            off = p - li * i_chunks;
+            const int total = nact * a.i_stages + a.is_stages;
+            p = (int)((uint32_t)(total * grp) / kGroups);
+            end = (int)((uint32_t)(total * (grp + 1)) / kGroups);
+            li = min((int)div_by(p, a.by_i_stages), nact);
+            off = p - li * a.i_stages;
         }
         while (p < end) {
             const bool routed = phase != 0 && li < nact;
             Unit u;
             u.e = routed ? s_list[li] : a.E;
             int c0 = 0, c1, took;
-            const int width = phase < 2 ? (routed ? a.I : a.Is) : (routed ? i_chunks : is_chunks);
+            const int width = phase < 2 ? (routed ? a.I : a.Is) : (routed ? a.i_stages : a.is_stages);
             if (phase < 2) {
                 took = u.n = min(min(kFeat, width - off), end - p);
                 u.f0 = off;
                 u.row0 = (routed ? (size_t)u.e * a.W1.rows : 0) + off;
                 u.row1 = u.row0 + (DUAL ? width : 8);
-                c1 = stages_of(a.H, a.sd);
+                c1 = a.up_stages;
             } else {
                 took = min(width - off, end - p);
                 u.n = nr;
@@ -594,22 +618,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 *s_abort = 1;
             }
         };
+        const int lw = a.T > 8 ? 0 : a.T > 4 ? 1 : a.T > 2 ? 2 : a.T > 1 ? 3 : 4;   // log2 of the warps per token
+        const int t = warp >> lw, ws = warp & ((1 << lw) - 1);   // this warp's token, and its share
         // ---- router: work item (expert, part of H); a warp takes one token's
         // row, or a share of it when there are fewer tokens than warps
         if (!a.logits) {
             F2* s_d = reinterpret_cast<F2*>(s_red);              // [kCw]
-            const int wpt = a.T > 8 ? 1 : a.T > 4 ? 2 : a.T > 2 ? 4 : a.T > 1 ? 8 : 16;   // warps per token
-            const int t = warp / wpt, ws = warp - t * wpt;
-            const int nq = a.H / 4;                              // groups of 4 k
+            const int nq = a.parts == 4 ? a.H >> 4 : a.parts == 2 ? a.H >> 3 : a.H >> 2;                    // groups of 4 k in a part (H is a multiple of 64)
             for (int it = cta; it < a.E * a.parts; it += G) {
-                const int e = it / a.parts, p = it - e * a.parts;
-                const int q1 = part(nq, p + 1, a.parts);
+                const int e = a.parts == 4 ? it >> 2 : a.parts == 2 ? it >> 1 : it, p = it - e * a.parts;
                 F2 acc{0.0f, 0.0f}, acc2{0.0f, 0.0f};
                 if (t < a.T)
 #pragma unroll 4
-                    for (int q = part(nq, p, a.parts) + ws * 32 + lane; q < q1; q += wpt * 32) {
-                        const float4 w = __ldg(reinterpret_cast<const float4*>(a.w_router + (size_t)e * a.H) + q);
-                        const uint2 v = *(reinterpret_cast<const uint2*>(a.x + (size_t)t * a.H) + q);
+                    for (int q = ws * 32 + lane; q < nq; q += 32 << lw) {
+                        const float4 w = __ldg(reinterpret_cast<const float4*>(a.w_router + (size_t)e * a.H) + p * nq + q);
+                        const uint2 v = *(reinterpret_cast<const uint2*>(a.x + (size_t)t * a.H) + p * nq + q);
                         fma_to(acc, w.x, bf16lo(v.x));
                         fma_to(acc2, w.y, bf16hi(v.x));
                         fma_to(acc, w.z, bf16lo(v.y));
@@ -622,10 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 named_bar(5, kCThreads);
                 if (warp == 0) {                                 // the warps of a token, by shuffles among 16 lanes
                     acc = s_d[lane & 15];
-                    for (int o = wpt >> 1; o > 0; o >>= 1)
+                    for (int o = (1 << lw) >> 1; o > 0; o >>= 1)
                         add_to(acc, F2{__shfl_xor_sync(0xffffffffu, acc.hi, o), __shfl_xor_sync(0xffffffffu, acc.lo, o)});
-                    const int tt = lane / wpt;
-                    if (lane < 16 && tt * wpt == lane && tt < a.T)
+                    const int tt = lane >> lw;
+                    if (lane < 16 && tt << lw == lane && tt < a.T)
                         __stcg(a.lg + ((size_t)p * a.T + tt) * a.E + e, make_float2(acc.hi, acc.lo));
                 }
                 if (it + G < a.E * a.parts) named_bar(5, kCThreads);
@@ -634,8 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
             if (tid == 0) arrive();
         }
         // ---- token rows into shared memory (while the other CTAs' logits arrive)
-        for (int i = tid; i < a.T * (a.H / 8); i += kCThreads) {
-            const int t = i / (a.H / 8), c = i - t * (a.H / 8);
+        if (t < a.T)
+#pragma unroll 4
+        for (int c = ws * 32 + lane; c < a.H / 8; c += 32 << lw) {
             uint4 v = *(reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H) + c);
             if (FMT != kBf16)                   // pairs (j, j + 4)
                 v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
@@ -645,28 +669,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         if (!a.logits && tid == 0) grid_wait();
         named_bar(5, kCThreads);
         // ---- selection: every CTA picks for all tokens, a warp per token
-        uint32_t* s_key = reinterpret_cast<uint32_t*>(s_red);          // [T][E]
+        uint32_t* s_key = reinterpret_cast<uint32_t*>(s_red);          // [T][Ep], zeros behind the experts
+        const int Ep = (a.E + 3) & ~3;
         for (int i = tid; i < a.T * a.E; i += kCThreads) {
-            const int t = i / a.E, e = i - t * a.E;
-            const F2 l2 = logit_f2(a, t, e);
+            const int tt = (int)div_by(i, a.by_E), e = i - tt * a.E;
+            const F2 l2 = logit_f2(a, tt, e);
             const float L = fabsf(l2.hi) <= 3.402823466e38f ? l2.hi + l2.lo : l2.hi;
-            s_key[i] = a.softmax ? __float_as_uint(L)
-                                 : key32(1.0f / (1.0f + expf(-L)) + (a.ebias ? __ldg(a.ebias + e) : 0.0f));
+            s_key[tt * Ep + e] = a.softmax ? __float_as_uint(L)
+                                           : key32(1.0f / (1.0f + expf(-L)) + (a.ebias ? __ldg(a.ebias + e) : 0.0f));
+            if (e == a.E - 1)
+                for (int q = a.E; q < Ep; ++q) s_key[tt * Ep + q] = 0u;
         }
         named_bar(5, kCThreads);
-        if (warp < a.T)
-            select_token(a, warp, s_key + warp * a.E, s_pick + warp * kMaxK, s_slot + warp * 256, s_mask);
-        named_bar(5, kCThreads);
-        if (warp == 0) {
-            int n = 0;
-            for (int e0 = 0; e0 < a.E; e0 += 32) {
-                const int e = e0 + lane;
-                const bool on = e < a.E && s_mask[e] != 0;
-                const uint32_t bal = __ballot_sync(0xffffffffu, on);
-                if (on) s_list[n + __popc(bal & ((1u << lane) - 1))] = e;
-                n += __popc(bal);
+        if (a.softmax) {
+            if (warp < a.T) softmax_keys(a, s_key + warp * Ep);
+            named_bar(5, kCThreads);
+        }
+        uint32_t* s_sorted = s_mask + kMaxE;                           // [T][kMaxK + 1]: keys by rank
+        const bool counted = a.T * a.E * a.E <= kMostCounted;
+        if (counted) {
+            // an expert's rank is the number of experts before it
+            for (int i = tid; i < a.T * a.E; i += kCThreads) {
+                const int tt = (int)div_by(i, a.by_E), e = i - tt * a.E;
+                const uint32_t* row = s_key + tt * Ep;
+                const uint32_t mine = row[e];
+                int rank = 0;
+#pragma unroll 4
+                for (int j = 0; j < Ep; j += 4) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(row + j);
+                    rank += (q.x > mine - (j < e)) + (q.y > mine - (j + 1 < e)) + (q.z > mine - (j + 2 < e)) +
+                            (q.w > mine - (j + 3 < e));
+                }
+                if (rank <= a.k) s_sorted[tt * (kMaxK + 1) + rank] = mine;
+                if (rank < a.k) s_pick[tt * kMaxK + rank] = e;
             }
-            if (lane == 0) {
+            named_bar(5, kCThreads);
+        }
+        if (warp < a.T)
+            select_token(a, warp, counted, s_key + warp * Ep, s_sorted + warp * (kMaxK + 1), s_pick + warp * kMaxK,
+                         s_slot + warp * 256, s_mask);
+        named_bar(5, kCThreads);
+        if (warp * 32 < a.E) {                  // the active experts, ascending: a warp per 32
+            int before = 0, n = 0;
+            uint32_t mine = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j * 32 < a.E) {
+                    const int e = j * 32 + lane;
+                    const uint32_t bal = __ballot_sync(0xffffffffu, e < a.E && s_mask[e] != 0);
+                    if (j < warp) before += __popc(bal);
+                    if (j == warp) mine = bal;
+                    n += __popc(bal);
+                }
+            if (mine >> lane & 1u) s_list[before + __popc(mine & ((1u << lane) - 1))] = warp * 32 + lane;
+            if (tid == 0) {
                 *s_nact = n;
                 s_mask[a.E] = (1u << a.T) - 1;
             }
@@ -716,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 for (int c = c0; c < c1; ++c) {
                     const int s = ring0 + slot, steps = min(sd.k, m.K - c * sd.k) / kStep;
                     const uint32_t st = ring + s * a.stage_bytes;
-                    const int s0 = steps * gw / kGw, n = steps * (gw + 1) / kGw - s0;
+                    const int s0 = (uint32_t)(steps * gw) / kGw, n = (uint32_t)(steps * (gw + 1)) / kGw - s0;
                     uint32_t xb[NT], sc0 = 0, sc1 = 0;
 #pragma unroll
                     for (int i = 0; i < NT; ++i) xb[i] = col[i] + (up ? c * sd.k * 2 : st) + s0 * (kStep * 2);
@@ -887,7 +943,16 @@ cudaError_t plan(Plan& p) {
     if (e == cudaSuccess && a.Is > 0) e = map(a.S2, a.S2.rows, c2);
     if (e != cudaSuccess) return e;
     // parts of the router's rows: work for all CTAs
-    a.parts = std::max(1, std::min(kMaxParts, di.sm_count / a.E));
+    a.parts = di.sm_count >= 4 * a.E ? 4 : di.sm_count >= 2 * a.E ? 2 : 1;
+    a.up_stages = (a.H + a.sd.k - 1) / a.sd.k;
+    a.i_stages = (a.I + a.sd2.k - 1) / a.sd2.k;
+    a.is_stages = (a.Is + a.sd2.k - 1) / a.sd2.k;
+    a.by_grid = divisor(di.sm_count);
+    a.by_groups = divisor(di.sm_count * kGroups);
+    a.by_I = divisor(a.I);
+    a.by_E = divisor(a.E);
+    a.by_i_stages = divisor(a.i_stages);
+    if ((uint64_t)a.E * a.I * (di.sm_count * kGroups + 1) >> 32) return cudaErrorNotSupported;   // part()
     p.smem = smem;
     p.grid = di.sm_count;
     p.launch = launch<FMT, NT, DUAL>;
