@@ -408,14 +408,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
     const int G = gridDim.x, cta = blockIdx.x;
     const int Sg = a.stages;                    // ring slots of one group (its own: it alone fills and frees them in order)
     for (int i = tid; i < kMaxE; i += kThreads) s_mask[i] = 0;
-    if (tid == 0) {
-        for (int i = 0; i < kGroups * Sg; ++i) {
-            mbar_init(&full[i], 2);             // weights, token rows
-            mbar_init(&empty[i], kGw);
-        }
-        *s_abort = 0;
+    if (tid < kGroups * Sg) {
+        mbar_init(&full[tid], 2);               // weights, token rows
+        mbar_init(&empty[tid], kGw);
         fence_mbar_init();
     }
+    if (tid == 0) *s_abort = 0;
     if (warp == kCw && lane < (a.Is > 0 ? 4 : 2))
         tma_prefetch_desc(lane == 0 ? &a.W1.map : lane == 1 ? &a.W2.map : lane == 2 ? &a.S1.map : &a.S2.map);
     __syncthreads();
@@ -604,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         // before, the other consumers wrote
         auto arrive = [&]() {
             asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(a.sync), "l"(1ull) : "memory");
-            target = (target ? target : seen - seen % (uint32_t)G) + (uint32_t)G;
+            target = (target ? target : __umul64hi(seen, a.by_grid.m) * (uint32_t)G) + (uint32_t)G;
         };
         auto grid_wait = [&]() {                // thread 0
             bool ok = false;
