@@ -110,8 +110,8 @@ struct Layout {                                 // shared memory (byte offsets)
     static constexpr int kPick = kList + 1040;                        // [kTok][kMaxK] expert of a pick
     static constexpr int kWt = kPick + kTok * kMaxK * 4;              // [kTok][kMaxK] routing weight
     static constexpr int kSlot = kWt + kTok * kMaxK * 4;              // [kTok][256] bytes: pick number of an expert
-    static constexpr int kMisc = kSlot + kTok * 256;                  // active count, abort flag
-    static constexpr int kBar = kMisc + 16;
+    static constexpr int kMisc = kSlot + kTok * 256;                  // active count, abort flag; maxima and scales of the token rows
+    static constexpr int kBar = kMisc + 16 + 2 * kCw * 4;
     static constexpr int kRed = kBar + 2 * kMaxStages * 8;            // group sums; later y sums per warp
     static constexpr int kRedBuf = kGw * kRows * kTok * 4;            // one buffer of one group
     static constexpr int kRedBytes = kGroups * 2 * kRedBuf;
@@ -396,13 +396,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
     float* s_wt = reinterpret_cast<float*>(sm + L::kWt);
     unsigned char* s_slot = sm + L::kSlot;
     int* s_nact = reinterpret_cast<int*>(sm + L::kMisc);
+    uint32_t* s_wmax = reinterpret_cast<uint32_t*>(sm + L::kMisc + 16);              // [kCw]
+    float* s_xinv = reinterpret_cast<float*>(sm + L::kMisc + 16 + kCw * 4);           // [kCw]: 1 / the tokens' scales
     volatile int* s_abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar);
     uint64_t* empty = full + kMaxStages;
     float* s_red = reinterpret_cast<float*>(sm + L::kRed);
     const int xstride = a.H * 2 + F::kXPad;
     const uint32_t xs = smem_u32(sm + L::kX);
-    const uint32_t ring = (xs + a.T * xstride + 1023) & ~1023u;     // swizzled boxes start on 1 KB
+    // affine: per group of 64 k and token (constant part of the products, sum of x)
+    float2* s_tab = reinterpret_cast<float2*>(sm + L::kX + a.T * xstride);
+    const uint32_t tab0 = xs + a.T * xstride;
+    const uint32_t ring = (tab0 + (FMT == kAffine ? a.H / 64 * a.T * 8 : 0) + 1023) & ~1023u;   // swizzled boxes start on 1 KB
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = gridDim.x, cta = blockIdx.x;
@@ -654,15 +659,65 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
             __syncwarp();
             if (tid == 0) arrive();
         }
-        // ---- token rows into shared memory (while the other CTAs' logits arrive)
-        if (t < a.T)
+        // ---- token rows into shared memory (while the other CTAs' logits arrive);
+        // 4-bit experts: in f16, scaled by a power of two that brings the row's
+        // largest finite value to [2^14, 2^15) (smaller values than 2^-29 of that
+        // lose bits to f16's subnormals; infinities and NaN stay)
+        float xscale = 1.0f;
+        if (FMT != kBf16) {
+            float m = 0.0f;
+            if (t < a.T)
 #pragma unroll 4
-        for (int c = ws * 32 + lane; c < a.H / 8; c += 32 << lw) {
-            uint4 v = *(reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H) + c);
-            if (FMT != kBf16)                   // pairs (j, j + 4)
-                v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                               __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-            *reinterpret_cast<uint4*>(sm + L::kX + (size_t)t * xstride + c * 16) = v;
+                for (int c = ws * 32 + lane; c < a.H / 8; c += 32 << lw) {
+                    const uint4 v = *(reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H) + c);
+                    const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float p = fabsf(bf16lo(r[i])), q = fabsf(bf16hi(r[i]));
+                        if (p < INFINITY) m = fmaxf(m, p);       // false for NaN
+                        if (q < INFINITY) m = fmaxf(m, q);
+                    }
+                }
+            const uint32_t mw = __reduce_max_sync(0xffffffffu, __float_as_uint(m));   // not negative: bits order as values
+            if (lane == 0) s_wmax[warp] = mw;
+            named_bar(5, kCThreads);
+            uint32_t mt = 0;
+            for (int i = 0; i < 1 << lw; ++i) mt = max(mt, s_wmax[(t << lw) + i]);
+            const int field = mt ? min(253, 268 - (int)(mt >> 23)) : 127;
+            xscale = __uint_as_float((uint32_t)field << 23);
+            if (ws == 0 && lane == 0) s_xinv[t] = __uint_as_float((uint32_t)(254 - field) << 23);
+        }
+        if (t < a.T) {
+            const int nc = a.H / 8;
+#pragma unroll 2
+            for (int c0 = ws * 32; c0 < nc; c0 += 32 << lw) {    // warp-uniform: lanes meet in shuffles below
+                const int c = c0 + lane;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (c < nc) v = *(reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H) + c);
+                if (FMT != kBf16) {
+                    float f[8] = {bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y),
+                                  bf16lo(v.z), bf16hi(v.z), bf16lo(v.w), bf16hi(v.w)};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] *= xscale;
+                    if (FMT == kNvfp4) {
+                        v = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
+                                       pack_f16x2(f[6], f[7]));
+                    } else {
+                        // pairs (j, j + 4); the odd pairs meet codes that count 16-fold
+                        v = make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f),
+                                       pack_f16x2(f[2], f[6]), pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f));
+                        const float e0 = (f[0] + f[4]) + (f[2] + f[6]), e1 = (f[1] + f[5]) + (f[3] + f[7]);
+                        float big = fmaf(1024.0f, e0, 64.0f * e1), sum = e0 + e1;
+#pragma unroll
+                        for (int o = 4; o > 0; o >>= 1) {        // 8 lanes hold the 64 k of a group
+                            big += __shfl_xor_sync(0xffffffffu, big, o);
+                            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                        }
+                        if ((lane & 7) == 0 && c < nc) s_tab[(c >> 3) * a.T + t] = make_float2(big, sum);
+                    }
+                }
+                if (c < nc) *reinterpret_cast<uint4*>(sm + L::kX + (size_t)t * xstride + c * 16) = v;
+            }
         }
         if (!a.logits && tid == 0) grid_wait();
         named_bar(5, kCThreads);
@@ -767,6 +822,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                     col[n] = (up ? xs + nth_bit(mask, c) * xstride : a.sd2.tokens + c * (a.sd2.k * 2 + F::kXPad)) +
                              t4 * (FMT == kBf16 ? 16 : 32);
                 }
+                uint32_t tcol[NT][2] = {};      // affine up: table entries of this lane's result columns
+                if (FMT == kAffine && up)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int c = n * 8 + 2 * t4 + q;
+                            tcol[n][q] = tab0 + nth_bit(mask, c < ncol ? c : 0) * 8;
+                        }
                 for (int c = c0; c < c1; ++c) {
                     const int s = ring0 + slot, steps = min(sd.k, m.K - c * sd.k) / kStep;
                     const uint32_t st = ring + s * a.stage_bytes;
@@ -788,7 +852,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                         }
                     }
                     if (!dead) {
-                        run_steps<FMT, NT>(st + sg * 128, sd.half, x4, s0, n, sc0, sc1, sd.area, xb, ntn, acc);
+                        if (FMT != kBf16 && up) {
+                            uint32_t tab[NT][2] = {};
+                            if (FMT == kAffine)
+#pragma unroll
+                                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                                    for (int q = 0; q < 2; ++q) tab[i][q] = tcol[i][q] + (c * (sd.k / 64) + s0) * a.T * 8;
+                            run_steps_f16<FMT, NT>(st + sg * 128, sd.half, x4, s0, n, sc0, sc1, sd.area, xb, tab, a.T * 8,
+                                                   ntn, acc);
+                        } else {
+                            run_steps<FMT, NT>(st + sg * 128, sd.half, x4, s0, n, sc0, sc1, sd.area, xb, ntn, acc);
+                        }
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&empty[s]);
@@ -797,8 +872,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                         ph ^= 1;
                     }
                 }
-                // NVFP4: the expert's global scale (the products carry 2^-8)
-                const float gl = FMT == kNvfp4 ? 256.0f * __ldg(m.glob + (u.e == a.E ? 0 : u.e)) : 1.0f;
+                // NVFP4: the expert's global scale (bf16 products carry 2^-8)
+                const float gl = FMT == kNvfp4 ? (up ? 1.0f : 256.0f) * __ldg(m.glob + (u.e == a.E ? 0 : u.e)) : 1.0f;
                 if (up) {
                     // the group's four k shares meet in shared memory
                     float* r = red + rbuf * (L::kRedBuf / 4);
@@ -820,9 +895,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                             v += r[(q * kRows + f) * TT + c];
                             if (DUAL) w += r[(q * kRows + 8 + f) * TT + c];
                         }
-                        if (FMT == kNvfp4) {
-                            v *= gl;
-                            w *= gl;
+                        if (FMT != kBf16) {
+                            const float sc = s_xinv[nth_bit(mask, c)] * (FMT == kNvfp4 ? gl : 1.0f);
+                            v *= sc;
+                            w *= sc;
                         }
                         if (DUAL) {
                             clamp_swiglu(v, w, u.e == a.E ? a.limit_s : a.limit);
@@ -911,7 +987,8 @@ cudaError_t plan(Plan& p) {
     const DeviceInfo& di = device_info();
     using F = Fmt<FMT>;
     // + 1 KB: the ring starts on a multiple of that
-    const size_t fixed = Layout<NT>::kX + (size_t)a.T * (a.H * 2 + F::kXPad) + 1024;
+    const size_t fixed =
+        Layout<NT>::kX + (size_t)a.T * (a.H * 2 + F::kXPad + (FMT == kAffine ? a.H / 8 : 0)) + 1024;
     const int room = fixed < (size_t)di.max_smem_optin ? (int)(di.max_smem_optin - fixed) : 0;
     // Two slots per group of 16 KB of weights each where they fit, smaller ones
     // (at last a single one) where the token rows leave less room.  Down stages

@@ -160,11 +160,11 @@ MOE_DEV uint32_t e4m3_to_bf16x2_118(uint32_t b) {
     return __float_as_uint(f) >> 16 | (__float_as_uint(f) & 0xFFFF0000u);
 }
 
-// The token operand of 4-bit steps holds, per 8 consecutive k, the pairs
-// (j, j + 4): element i of the 8 goes to position 2 (i % 4) + i / 4.
+// The token operand of bf16 4-bit steps (and of affine f16 ones) holds, per 8
+// consecutive k, the pairs (j, j + 4): element i of the 8 goes to position 2 (i % 4) + i / 4.
 MOE_DEV int pair_pos(int k) { return (k & ~7) | (((k & 3) << 1) | ((k >> 2) & 1)); }
 
-// The products of steps [s, s + n) of a stage.  w: this lane's row of half 0
+// The products of steps [s, s + n) of a stage, token operand in bf16.  w: this lane's row of half 0
 // (stage + sigma 128), half 1 at + half; x4: the lane's 16-byte unit, XORed by
 // the row; sc0, sc1: the scales of its two rows at the first step; xb: this
 // lane's k of its column, per block of 8 tokens, at the first step.
@@ -253,6 +253,98 @@ MOE_DEV void run_steps(uint32_t w, uint32_t half, uint32_t x4, int s, int n, uin
                 }
         }
     }
+}
+
+MOE_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 4-bit steps with the token operand in f16 (x after a power-of-two scale per
+// token).  A step costs 75-90 issue cycles per warp instead of ~135 with bf16:
+// integer and shift instructions issue at half rate, and f16 needs fewer.
+//   NVFP4   the e2m1 pairs and block scales convert by instruction, their f16
+//           product is exact; x in natural order.
+//   affine  in f16, 1024 + q and 1024 + 16 q are exact for a nibble at bits 0-3
+//           and 4-7 of a half: two pairs of codes per shift.  The second kind meets
+//           x / 16, and the products start at minus their constant part:
+//             sum_k q x = sum (1024 + q) x + sum (1024 + 16 q) (x / 16) - O,
+//           O = 1024 (sum x + sum x / 16) over the respective k, from a table of
+//           (O, sum x) per group of 64 and token.  O is up to ~100 times the
+//           result, so a group's sum is good to ~1e-5 of itself: far inside the
+//           bf16 rounding of the activations.
+// tab: this lane's columns 2t and 2t + 1 of each block of 8 in the table at the
+// first step; tstep: bytes from one group to the next.
+template <int FMT, int NT>
+MOE_DEV void run_steps_f16(uint32_t w, uint32_t half, uint32_t x4, int s, int n, uint32_t sc0, uint32_t sc1, uint32_t area,
+                           uint32_t (&xb)[NT], uint32_t (&tab)[NT][2], uint32_t tstep, int ntn, float (&acc)[NT][4]) {
+    if constexpr (FMT == kNvfp4) {
+#pragma unroll(NT == 1 ? 4 : 2)
+        for (; n > 0; --n, ++s, sc0 += 4, sc1 += 4) {
+            const uint32_t a = w + ((s & ~3) << 8) + (((s << 5) & 0x60) ^ x4);
+            const uint2 p = lds64(a), q = lds64(a + half);
+            const uint32_t s0 = e4m3x2_to_f16x2(lds_u8(sc0) * 0x0101u), s1 = e4m3x2_to_f16x2(lds_u8(sc1) * 0x0101u);
+            uint32_t f[2][4], h[2][4];
+            e2m1x8_to_f16(p.x, f[0]);
+            e2m1x8_to_f16(q.x, h[0]);
+            e2m1x8_to_f16(p.y, f[1]);
+            e2m1x8_to_f16(q.y, h[1]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                f[j >> 2][j & 3] = hmul2_u32(f[j >> 2][j & 3], s0);
+                h[j >> 2][j & 3] = hmul2_u32(h[j >> 2][j & 3], s1);
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                if (i == 0 || i < ntn) {
+                    const uint4 u = lds128(xb[i]), v = lds128(xb[i] + 16);
+                    xb[i] += 128;
+                    mma_f16(acc[i], f[0][0], h[0][0], f[0][1], h[0][1], u.x, u.y);
+                    mma_f16(acc[i], f[0][2], h[0][2], f[0][3], h[0][3], u.z, u.w);
+                    mma_f16(acc[i], f[1][0], h[1][0], f[1][1], h[1][1], v.x, v.y);
+                    mma_f16(acc[i], f[1][2], h[1][2], f[1][3], h[1][3], v.z, v.w);
+                }
+        }
+    } else {
+        const auto lo = [](uint32_t v) { return (v & 0x000F000Fu) | 0x64006400u; };
+        const auto hi = [](uint32_t v) { return (v & 0x00F000F0u) | 0x64006400u; };
+#pragma unroll 2
+        for (; n > 0; --n, ++s, sc0 += 2, sc1 += 2) {
+            const uint32_t a = w + ((s & ~3) << 8) + (((s << 5) & 0x60) ^ x4);
+            const uint2 p = lds64(a), q = lds64(a + half);
+            const float s0 = bf16f(lds_u16(sc0)), s1 = bf16f(lds_u16(sc1));
+            const float b0 = bf16f(lds_u16(sc0 + area)), b1 = bf16f(lds_u16(sc1 + area));
+            const uint32_t px = p.x >> 8, qx = q.x >> 8, py = p.y >> 8, qy = q.y >> 8;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                if (i == 0 || i < ntn) {
+                    const uint4 u = lds128(xb[i]), v = lds128(xb[i] + 16);
+                    const uint2 t0 = lds64(tab[i][0]), t1 = lds64(tab[i][1]);   // (O, sum x) of the two columns
+                    xb[i] += 128;
+                    tab[i][0] += tstep;
+                    tab[i][1] += tstep;
+                    float c[4];
+                    c[0] = c[2] = -__uint_as_float(t0.x);
+                    c[1] = c[3] = -__uint_as_float(t1.x);
+                    mma_f16(c, lo(p.x), lo(q.x), hi(p.x), hi(q.x), u.x, u.y);
+                    mma_f16(c, lo(px), lo(qx), hi(px), hi(qx), u.z, u.w);
+                    mma_f16(c, lo(p.y), lo(q.y), hi(p.y), hi(q.y), v.x, v.y);
+                    mma_f16(c, lo(py), lo(qy), hi(py), hi(qy), v.z, v.w);
+                    const float x0 = __uint_as_float(t0.y), x1 = __uint_as_float(t1.y);
+                    acc[i][0] = fmaf(s0, c[0], fmaf(b0, x0, acc[i][0]));
+                    acc[i][1] = fmaf(s0, c[1], fmaf(b0, x1, acc[i][1]));
+                    acc[i][2] = fmaf(s1, c[2], fmaf(b1, x0, acc[i][2]));
+                    acc[i][3] = fmaf(s1, c[3], fmaf(b1, x1, acc[i][3]));
+                }
+        }
+    }
+}
+
+MOE_DEV uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 }  // namespace stream
