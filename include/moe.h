@@ -338,7 +338,7 @@ typedef struct {
  * moe_decode is prepare and run.  A run on another device than the plan's is
  * MOE_ERR_UNSUPPORTED. */
 typedef struct {
-    uint64_t opaque[192];
+    uint64_t opaque[384];
 } moe_decode_plan;
 MOE_API moe_status moe_decode_prepare(const moe_layer* L, const moe_dims* d, moe_decode_plan* plan);
 MOE_API moe_status moe_decode_run(const moe_decode_plan* plan, const void* x, const float* logits,

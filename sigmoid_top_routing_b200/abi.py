@@ -63,7 +63,7 @@ class moe_layer(ctypes.Structure):
 
 
 class moe_decode_plan(ctypes.Structure):
-    _fields_ = [("opaque", ctypes.c_uint64 * 192)]
+    _fields_ = [("opaque", ctypes.c_uint64 * 384)]
 
 
 class moe_linear_dims(ctypes.Structure):

@@ -58,7 +58,9 @@ constexpr int kMaxParts = 4;                    // parts of a router row
 
 struct WMat {                                   // one weight tensor of the experts
     CUtensorMap map;                            // (experts * rows) rows of codes
+    CUtensorMap smap, bmap;                     // boxes of their scales and biases, when boxed
     bool flat;                                  // rows are not whole 128-byte chunks
+    bool boxed;
     const unsigned char* w;
     const unsigned char* scale;
     const unsigned char* bias;
@@ -311,7 +313,7 @@ struct Unit {
     int e;                                      // expert; a.E: the shared one
     int n;                                      // features (up) or rows (down): rows of both halves, or of each when dual
     int f0;                                     // first feature (up) or row of y (down)
-    size_t row0, row1;                          // first weight row of either half of 8 rows
+    int row0, row1;                             // first weight row of either half of 8 rows
 };
 
 // Start of part i of d.n equal parts of v (v * i below 2^32: at most 256 experts
@@ -327,7 +329,7 @@ MOE_DEV void issue_weights(const StageDims& sd, const WMat& m, const Unit& u, bo
     const bool two = dual || u.n > 8;           // else the second half's rows are nobody's
     uint32_t sb = 0, sdst = 0;
     size_t s0 = 0;
-    if (FMT != kBf16) {
+    if (FMT != kBf16 && !m.boxed) {
         // scale rows start anywhere: copy the 16-byte aligned span around them
         // (the arrays hold a multiple of 128 bytes, so it stays inside)
         const size_t SB = F::scale_bytes(m.K);
@@ -335,7 +337,7 @@ MOE_DEV void issue_weights(const StageDims& sd, const WMat& m, const Unit& u, bo
         if (m.K <= kSpanMaxK) {                 // whole rows: one span per half
             const int n = dual ? u.n : lane == 0 ? min(u.n, 8) : u.n - 8;
             if (lane < 2 && n > 0) {
-                b = (lane ? u.row1 : u.row0) * SB;
+                b = (size_t)(lane ? u.row1 : u.row0) * SB;
                 e = b + n * SB;
                 sdst = lane * (sd.area / 2);
             }
@@ -343,7 +345,7 @@ MOE_DEV void issue_weights(const StageDims& sd, const WMat& m, const Unit& u, bo
             const int loc = lane & 7, n = dual || lane < 8 ? min(u.n, 8) : u.n - 8;
             if (loc < n) {
                 const int k0 = c * sd.k;
-                b = ((lane >= 8 ? u.row1 : u.row0) + loc) * SB + F::scale_bytes(k0);
+                b = (size_t)((lane >= 8 ? u.row1 : u.row0) + loc) * SB + F::scale_bytes(k0);
                 e = b + F::scale_bytes(min(sd.k, m.K - k0));
                 sdst = lane * (sd.area / kRows);
             }
@@ -353,11 +355,20 @@ MOE_DEV void issue_weights(const StageDims& sd, const WMat& m, const Unit& u, bo
             sb = (uint32_t)(((e + 15) & ~size_t(15)) - s0);
         }
     }
-    const uint32_t total = (two ? 2u : 1u) * sd.half + (FMT == kBf16 ? 0u : __reduce_add_sync(0xffffffffu, sb)) * (FMT == kAffine ? 2 : 1);
+    uint32_t total = (two ? 2u : 1u) * sd.half;
+    if (FMT != kBf16)
+        total += (FMT == kAffine ? 2u : 1u) *
+                 (m.boxed ? (two ? 2u : 1u) * 8 * F::kScaleBox : __reduce_add_sync(0xffffffffu, sb));
     if (lane == 0) mbar_arrive_expect_tx(bar, total);
     __syncwarp();
     if (lane < (two ? 2 : 1)) {
-        const int row = (int)(lane ? u.row1 : u.row0);
+        const int row = lane ? u.row1 : u.row0;
+        if (FMT != kBf16 && m.boxed) {
+            const int x = c * (int)F::scale_bytes(sd.k);
+            const uint32_t to = dst + sd.scales + lane * (sd.area / 2);
+            tma_load_rows(to, &m.smap, x, row, bar, pol);
+            if (FMT == kAffine) tma_load_rows(to + sd.area, &m.bmap, x, row, bar, pol);
+        }
         if (!m.flat) {
             tma_load_3d(dst + lane * sd.half, &m.map, row, c * sd.chunks, bar, pol);
         } else {
@@ -371,16 +382,16 @@ MOE_DEV void issue_weights(const StageDims& sd, const WMat& m, const Unit& u, bo
     }
 }
 
-// Stage address of the scales of row `loc` of a half, at the first step of stage c.
+// Stage address of the scales of row `loc` of a half at stage c (its first byte,
+// before the swizzle's term).
 template <int FMT>
 MOE_DEV uint32_t scale_addr(const StageDims& sd, const WMat& m, const Unit& u, int half, int loc, int c, uint32_t st) {
     using F = Fmt<FMT>;
-    const size_t base = half ? u.row1 : u.row0;
-    const size_t SB = F::scale_bytes(m.K);
-    if (m.K <= kSpanMaxK)
-        return st + sd.scales + half * (sd.area / 2) + uint32_t((base * SB) & 15) + loc * (uint32_t)SB +
-               (uint32_t)F::scale_bytes(c * sd.k);
-    return st + sd.scales + (half * 8 + loc) * (sd.area / kRows) + uint32_t(((base + loc) * SB + F::scale_bytes(c * sd.k)) & 15);
+    if (m.boxed) return st + sd.scales + half * (sd.area / 2) + loc * F::kScaleBox;
+    // only the low 4 bits of the global byte count: 32-bit products do
+    const uint32_t base = half ? u.row1 : u.row0, SB = (uint32_t)F::scale_bytes(m.K), o = (uint32_t)F::scale_bytes(c * sd.k);
+    if (m.K <= kSpanMaxK) return st + sd.scales + half * (sd.area / 2) + ((base * SB) & 15) + loc * SB + o;
+    return st + sd.scales + (half * 8 + loc) * (sd.area / kRows) + (((base + loc) * SB + o) & 15);
 }
 
 template <int FMT, int NT, bool DUAL>
@@ -471,14 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
             if (phase < 2) {
                 took = u.n = min(min(kFeat, width - off), end - p);
                 u.f0 = off;
-                u.row0 = (routed ? (size_t)u.e * a.W1.rows : 0) + off;
+                u.row0 = (routed ? u.e * a.W1.rows : 0) + off;
                 u.row1 = u.row0 + (DUAL ? width : 8);
                 c1 = a.up_stages;
             } else {
                 took = min(width - off, end - p);
                 u.n = nr;
                 u.f0 = r0;
-                u.row0 = (routed ? (size_t)u.e * a.H : 0) + r0;
+                u.row0 = (routed ? u.e * a.H : 0) + r0;
                 u.row1 = u.row0 + 8;
                 c0 = off;
                 c1 = off + took;
@@ -835,13 +846,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                     const int s = ring0 + slot, steps = min(sd.k, m.K - c * sd.k) / kStep;
                     const uint32_t st = ring + s * a.stage_bytes;
                     const int s0 = (uint32_t)(steps * gw) / kGw, n = (uint32_t)(steps * (gw + 1)) / kGw - s0;
-                    uint32_t xb[NT], sc0 = 0, sc1 = 0;
+                    uint32_t xb[NT], sc0 = 0, sc1 = 0, sb = 0, sx = 0;
 #pragma unroll
                     for (int i = 0; i < NT; ++i) xb[i] = col[i] + (up ? c * sd.k * 2 : st) + s0 * (kStep * 2);
                     if (FMT != kBf16) {
-                        const uint32_t o = s0 * (FMT == kAffine ? 2 : 4) + (FMT == kNvfp4 ? t4 : 0);
-                        sc0 = scale_addr<FMT>(sd, m, u, 0, sg, c, st) + o;
-                        sc1 = scale_addr<FMT>(sd, m, u, 1, sg, c, st) + o;
+                        sb = s0 * (FMT == kAffine ? 2 : 4) + (FMT == kNvfp4 ? t4 : 0);
+                        sx = !m.boxed ? 0 : FMT == kNvfp4 ? sg << 4 : (sg >> 1) << 4;
+                        sc0 = scale_addr<FMT>(sd, m, u, 0, sg, c, st);
+                        sc1 = scale_addr<FMT>(sd, m, u, 1, sg, c, st);
                     }
                     if (!dead) {
                         const bool got = mbar_wait(&full[s], ph, s_abort, a.wait_limit);
@@ -859,10 +871,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                                 for (int i = 0; i < NT; ++i)
 #pragma unroll
                                     for (int q = 0; q < 2; ++q) tab[i][q] = tcol[i][q] + (c * (sd.k / 64) + s0) * a.T * 8;
-                            run_steps_f16<FMT, NT>(st + sg * 128, sd.half, x4, s0, n, sc0, sc1, sd.area, xb, tab, a.T * 8,
+                            run_steps_f16<FMT, NT>(st + sg * 128, sd.half, x4, s0, n, sc0, sc1, sb, sx, sd.area, xb, tab, a.T * 8,
                                                    ntn, acc);
                         } else {
-                            run_steps<FMT, NT>(st + sg * 128, sd.half, x4, s0, n, sc0, sc1, sd.area, xb, ntn, acc);
+                            run_steps<FMT, NT>(st + sg * 128, sd.half, x4, s0, n, sc0, sc1, sb, sx, sd.area, xb, ntn, acc);
                         }
                     }
                     __syncwarp();
@@ -998,8 +1010,9 @@ cudaError_t plan(Plan& p) {
     int slots = 3, c1, c2;
     do {
         const int most = room / (--slots * kGroups);
-        for (c1 = 8; c1 > 1 && up(c1).bytes > most;) --c1;
-        for (c2 = 8; c2 > 1 && down(c2).bytes > most;) --c2;
+        // (affine: even numbers, for scale boxes on 16-byte starts)
+        for (c1 = 8; c1 > 1 && up(c1).bytes > most;) c1 -= FMT == kAffine && c1 > 2 ? 2 : 1;
+        for (c2 = 8; c2 > 1 && down(c2).bytes > most;) c2 -= FMT == kAffine && c2 > 2 ? 2 : 1;
     } while (slots > 1 && (c1 == 1 || c2 == 1));
     a.sd = up(c1);
     a.sd2 = down(c2);
@@ -1010,7 +1023,13 @@ cudaError_t plan(Plan& p) {
     const int n1 = a.E * a.W1.rows, n2 = a.E * a.W2.rows;
     auto map = [&](WMat& m, int rows, int chunks) {
         const uint64_t bytes = FMT == kBf16 ? (uint64_t)m.K * 2 : (uint64_t)m.K / 2;
-        return make_tmap_rows(&m.map, m.w, bytes, bytes, rows, 8, chunks, &m.flat);
+        cudaError_t e = make_tmap_rows(&m.map, m.w, bytes, bytes, rows, 8, chunks, &m.flat);
+        m.boxed = F::boxed(chunks, m.K);
+        if (e == cudaSuccess && m.boxed)
+            e = make_tmap_narrow(&m.smap, m.scale, F::scale_bytes(m.K), rows, F::kScaleBox);
+        if (e == cudaSuccess && m.boxed && FMT == kAffine)
+            e = make_tmap_narrow(&m.bmap, m.bias, F::scale_bytes(m.K), rows, F::kScaleBox);
+        return e;
     };
     cudaError_t e = map(a.W1, n1, c1);
     if (e == cudaSuccess) e = map(a.W2, n2, c2);

@@ -41,8 +41,8 @@ constexpr int kSpanMaxK = 4096;                       // 4-bit: longest row whos
 struct StageDims {
     int chunks, k;                                    // chunks and k of a row in one stage
     int half;                                         // bytes of a half's codes
-    int area;                                         // 4-bit: bytes of one scale array (affine has two): a span
-                                                      // per half at area / 2, or 16 row slots of area / 16
+    int area;                                         // 4-bit: bytes of one scale array (affine has two): a box or
+                                                      // span per half at area / 2, or 16 row slots of area / 16
     int scales, tokens;                               // byte offsets of the scales and of the token rows
     int bytes;
 };
@@ -56,11 +56,20 @@ struct Fmt {
     static MOE_DEV __host__ int sigma(int g) { return FMT == kBf16 ? (g >> 1) | ((g & 1) << 2) : ((g & 3) << 1) | (g >> 2); }
     // bytes of the scales of k weights (each array)
     static MOE_DEV __host__ size_t scale_bytes(int k) { return FMT == kAffine ? (size_t)k / 32 : (size_t)k / 16; }
-    // Bytes of one scale array of a stage of k, for rows of length K.
-    static int scale_area(int k, int K) {
+    // Scales of a stage arrive as one box per half (8 rows x 128 bytes NVFP4, 64
+    // affine) in the swizzle of that width where their rows are whole 16-byte units
+    // and a stage starts on one: the 8 rows of a load phase then fall on distinct
+    // banks (as plain spans, rows of 64 or 128 bytes cost 4 or 8 wavefronts a load).
+    static constexpr int kScaleBox = FMT == kAffine ? 64 : 128;
+    static bool boxed(int chunks, int K) {
+        return FMT == kNvfp4 ? K % 256 == 0 : FMT == kAffine && K % 512 == 0 && chunks % 2 == 0;
+    }
+    // Bytes of one scale array of a stage, for rows of length K.
+    static int scale_area(int chunks, int K) {
         if (FMT == kBf16 || K == 0) return 0;
+        if (boxed(chunks, K)) return 2 * 8 * kScaleBox;
         if (K <= kSpanMaxK) return 2 * (int)((8 * scale_bytes(K) + 32 + 15) & ~size_t(15));
-        return kRows * (int)((scale_bytes(k) + 32 + 15) & ~size_t(15));
+        return kRows * (int)((scale_bytes(chunks * kChunkK) + 32 + 15) & ~size_t(15));
     }
     // A stage for rows of length K1 or K2 with `cols` token rows behind the weights.
     static StageDims dims(int chunks, int K1, int K2, int cols) {
@@ -69,7 +78,8 @@ struct Fmt {
         d.k = chunks * kChunkK;
         d.half = chunks * 1024;
         d.scales = 2 * d.half;
-        d.area = scale_area(d.k, K1) > scale_area(d.k, K2) ? scale_area(d.k, K1) : scale_area(d.k, K2);
+        const int a1 = scale_area(chunks, K1), a2 = scale_area(chunks, K2);
+        d.area = ((a1 > a2 ? a1 : a2) + 1023) & ~1023;   // both arrays and halves start on a swizzle period
         d.tokens = d.scales + (FMT == kAffine ? 2 * d.area : d.area);
         d.bytes = (d.tokens + cols * (d.k * 2 + kXPad) + 1023) & ~1023;
         return d;
@@ -166,10 +176,10 @@ MOE_DEV int pair_pos(int k) { return (k & ~7) | (((k & 3) << 1) | ((k >> 2) & 1)
 
 // The products of steps [s, s + n) of a stage, token operand in bf16.  w: this lane's row of half 0
 // (stage + sigma 128), half 1 at + half; x4: the lane's 16-byte unit, XORed by
-// the row; sc0, sc1: the scales of its two rows at the first step; xb: this
-// lane's k of its column, per block of 8 tokens, at the first step.
+// the row; sc0, sc1: the scale rows of its two rows, read at byte sb ^ sx (sb: this
+// step's, sx: the swizzle's term of the row); xb: this lane's k of its column, per block of 8 tokens, at the first step.
 template <int FMT, int NT>
-MOE_DEV void run_steps(uint32_t w, uint32_t half, uint32_t x4, int s, int n, uint32_t sc0, uint32_t sc1, uint32_t area,
+MOE_DEV void run_steps(uint32_t w, uint32_t half, uint32_t x4, int s, int n, uint32_t sc0, uint32_t sc1, uint32_t sb, uint32_t sx, uint32_t area,
                        uint32_t (&xb)[NT], int ntn, float (&acc)[NT][4]) {
     if constexpr (FMT == kBf16) {
         w += s * 1024;
@@ -192,12 +202,13 @@ MOE_DEV void run_steps(uint32_t w, uint32_t half, uint32_t x4, int s, int n, uin
         // sum_k w x = s sum_k (128 + q) x + (b - 128 s) sum_k x over the step,
         // which is one group of 64; sum_k x by MMAs against ones
 #pragma unroll 1
-        for (; n > 0; --n, ++s, sc0 += 2, sc1 += 2) {
+        for (; n > 0; --n, ++s, sb += 2) {
             const uint32_t a = w + ((s & ~3) << 8) + (((s << 5) & 0x60) ^ x4);
             const uint2 p = lds64(a), q = lds64(a + half);
-            const float s0 = bf16f(lds_u16(sc0)), s1 = bf16f(lds_u16(sc1));
-            const float b0 = fmaf(-128.0f, s0, bf16f(lds_u16(sc0 + area)));
-            const float b1 = fmaf(-128.0f, s1, bf16f(lds_u16(sc1 + area)));
+            const uint32_t o0 = sc0 + (sb ^ sx), o1 = sc1 + (sb ^ sx);
+            const float s0 = bf16f(lds_u16(o0)), s1 = bf16f(lds_u16(o1));
+            const float b0 = fmaf(-128.0f, s0, bf16f(lds_u16(o0 + area)));
+            const float b1 = fmaf(-128.0f, s1, bf16f(lds_u16(o1 + area)));
             constexpr uint32_t one = 0x3F803F80u;
 #pragma unroll
             for (int i = 0; i < NT; ++i)
@@ -222,10 +233,10 @@ MOE_DEV void run_steps(uint32_t w, uint32_t half, uint32_t x4, int s, int n, uin
     } else {
         // a lane's 16 k are one scale block: e2m1 * e4m3 exactly in bf16, times 2^-8
 #pragma unroll 1
-        for (; n > 0; --n, ++s, sc0 += 4, sc1 += 4) {
+        for (; n > 0; --n, ++s, sb += 4) {
             const uint32_t a = w + ((s & ~3) << 8) + (((s << 5) & 0x60) ^ x4);
             const uint2 p = lds64(a), q = lds64(a + half);
-            const uint32_t s0 = e4m3_to_bf16x2_118(lds_u8(sc0)), s1 = e4m3_to_bf16x2_118(lds_u8(sc1));
+            const uint32_t s0 = e4m3_to_bf16x2_118(lds_u8(sc0 + (sb ^ sx))), s1 = e4m3_to_bf16x2_118(lds_u8(sc1 + (sb ^ sx)));
             uint4 u[NT], v[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i)
@@ -278,14 +289,15 @@ MOE_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
 // tab: this lane's columns 2t and 2t + 1 of each block of 8 in the table at the
 // first step; tstep: bytes from one group to the next.
 template <int FMT, int NT>
-MOE_DEV void run_steps_f16(uint32_t w, uint32_t half, uint32_t x4, int s, int n, uint32_t sc0, uint32_t sc1, uint32_t area,
+MOE_DEV void run_steps_f16(uint32_t w, uint32_t half, uint32_t x4, int s, int n, uint32_t sc0, uint32_t sc1, uint32_t sb, uint32_t sx, uint32_t area,
                            uint32_t (&xb)[NT], uint32_t (&tab)[NT][2], uint32_t tstep, int ntn, float (&acc)[NT][4]) {
     if constexpr (FMT == kNvfp4) {
 #pragma unroll(NT == 1 ? 4 : 2)
-        for (; n > 0; --n, ++s, sc0 += 4, sc1 += 4) {
+        for (; n > 0; --n, ++s, sb += 4) {
             const uint32_t a = w + ((s & ~3) << 8) + (((s << 5) & 0x60) ^ x4);
             const uint2 p = lds64(a), q = lds64(a + half);
-            const uint32_t s0 = e4m3x2_to_f16x2(lds_u8(sc0) * 0x0101u), s1 = e4m3x2_to_f16x2(lds_u8(sc1) * 0x0101u);
+            const uint32_t s0 = e4m3x2_to_f16x2(lds_u8(sc0 + (sb ^ sx)) * 0x0101u),
+                           s1 = e4m3x2_to_f16x2(lds_u8(sc1 + (sb ^ sx)) * 0x0101u);
             uint32_t f[2][4], h[2][4];
             e2m1x8_to_f16(p.x, f[0]);
             e2m1x8_to_f16(q.x, h[0]);
@@ -311,11 +323,12 @@ MOE_DEV void run_steps_f16(uint32_t w, uint32_t half, uint32_t x4, int s, int n,
         const auto lo = [](uint32_t v) { return (v & 0x000F000Fu) | 0x64006400u; };
         const auto hi = [](uint32_t v) { return (v & 0x00F000F0u) | 0x64006400u; };
 #pragma unroll 2
-        for (; n > 0; --n, ++s, sc0 += 2, sc1 += 2) {
+        for (; n > 0; --n, ++s, sb += 2) {
             const uint32_t a = w + ((s & ~3) << 8) + (((s << 5) & 0x60) ^ x4);
             const uint2 p = lds64(a), q = lds64(a + half);
-            const float s0 = bf16f(lds_u16(sc0)), s1 = bf16f(lds_u16(sc1));
-            const float b0 = bf16f(lds_u16(sc0 + area)), b1 = bf16f(lds_u16(sc1 + area));
+            const uint32_t o0 = sc0 + (sb ^ sx), o1 = sc1 + (sb ^ sx);
+            const float s0 = bf16f(lds_u16(o0)), s1 = bf16f(lds_u16(o1));
+            const float b0 = bf16f(lds_u16(o0 + area)), b1 = bf16f(lds_u16(o1 + area));
             const uint32_t px = p.x >> 8, qx = q.x >> 8, py = p.y >> 8, qy = q.y >> 8;
 #pragma unroll
             for (int i = 0; i < NT; ++i)

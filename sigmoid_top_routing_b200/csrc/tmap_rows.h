@@ -18,4 +18,8 @@ namespace moe {
 cudaError_t make_tmap_rows(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t stride, uint64_t rows,
                            uint32_t box_rows, uint32_t box_chunks, bool* flat);
 
+// 2D map of the same rows for boxes of 8 rows x box_bytes (64 or 128) bytes in
+// the swizzle of that width; row_bytes and stride are multiples of 16.
+cudaError_t make_tmap_narrow(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_bytes);
+
 }  // namespace moe
