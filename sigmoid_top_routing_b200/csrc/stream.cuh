@@ -143,8 +143,16 @@ MOE_DEV void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// (v & m) | o in one instruction with both constants in registers (written as
+// an expression, the two constants became two instructions: an affine f16 step
+// took 475 instead of 360 cycles at 16 warps).
+MOE_DEV uint32_t and_or(uint32_t v, uint32_t m, uint32_t o) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(m), "r"(o));
+    return r;
+}
 // Affine codes: nibbles j and j + 4 of v as the bf16 pair (128 + q_j, 128 + q_{j+4}), exact.
-MOE_DEV uint32_t nib_pair(uint32_t v, int j) { return ((v >> (4 * j)) & 0x000F000Fu) | 0x43004300u; }
+MOE_DEV uint32_t nib_pair(uint32_t v, int j) { return and_or(v >> (4 * j), 0x000F000Fu, 0x43004300u); }
 
 // e2m1 codes (nibbles j and j + 4 of w, j = 0..3) times a block scale, as bf16
 // pairs.  A code's exponent and mantissa bits at bits 8..6 of a bf16 are its
@@ -320,8 +328,8 @@ MOE_DEV void run_steps_f16(uint32_t w, uint32_t half, uint32_t x4, int s, int n,
                 }
         }
     } else {
-        const auto lo = [](uint32_t v) { return (v & 0x000F000Fu) | 0x64006400u; };
-        const auto hi = [](uint32_t v) { return (v & 0x00F000F0u) | 0x64006400u; };
+        const auto lo = [](uint32_t v) { return and_or(v, 0x000F000Fu, 0x64006400u); };
+        const auto hi = [](uint32_t v) { return and_or(v, 0x00F000F0u, 0x64006400u); };
 #pragma unroll 2
         for (; n > 0; --n, ++s, sb += 2) {
             const uint32_t a = w + ((s & ~3) << 8) + (((s << 5) & 0x60) ^ x4);
