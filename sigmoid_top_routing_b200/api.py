@@ -285,7 +285,7 @@ def moe_linear(x, w, bias=None, residual=None, *, act: str = "none", swiglu_limi
         ldr = _rows("residual", residual, M, N, _OUT, dev)
         res_p, res_f32 = residual.data_ptr(), residual.dtype is torch.float32
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
+        y = x.new_empty((M, N), dtype=out_dtype)   # (None: x's bf16)
         if y.dtype not in _OUT:
             raise ValueError(f"out_dtype: expected bfloat16 or float32, got {out_dtype}")
         ldy = N

@@ -42,8 +42,7 @@ using namespace sm100;
 
 constexpr int kBK = 64;                          // k per stage: one 128-byte swizzle row
 constexpr int kAStage = 128 * kBK * 2;           // 16 KB of weight rows per CTA
-constexpr int kLinThreads = 192;                 // producer, MMA issuer, 4 epilogue warps (split)
-constexpr int kPairThreads = 320;                // ... 8 epilogue warps, two per TMEM quarter (pair)
+constexpr int kLinThreads = 320;                 // producer, MMA issuer, 8 epilogue warps (two per TMEM quarter)
 constexpr int kMaxStage = 8;
 constexpr int kMaxKs = 8;                        // CTAs that share a tile's K
 
@@ -202,7 +201,7 @@ constexpr int kPairMaxStages = 5;
 constexpr size_t kPairSmem = size_t(kPairRing) + 1024 + 256;
 
 template <int ACT>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kLinThreads, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, LinParams p) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm =
@@ -493,9 +492,10 @@ __global__ void __launch_bounds__(kLinThreads)
     float b0, b1;
     bias_of<ACT>(p, f, b0, b1);
     const uint32_t tb = tmem + (uint32_t(32 * sub) << 16);
+    const int half = warp < 6 ? 0 : 1;           // the two warps of a TMEM quarter share its columns
     if (p.ks == 1) {
         if (warp >= 2 && !dead)
-            for (int c = 0; c < nc; c += 16) {
+            for (int c = half * 16; c < nc; c += 32) {
                 float v[16];
                 tmem_ld16(tb + c, v);
                 emit<ACT, 16>(p, v, f, t0 + c, b0, b1);
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kLinThreads)
     } else {
         float* part = reinterpret_cast<float*>(sm);              // [BN][128], over the stages
         if (warp >= 2)
-            for (int c = 0; c < nc; c += 16) {
+            for (int c = half * 16; c < nc; c += 32) {
                 float v[16];
                 tmem_ld16(tb + c, v);
 #pragma unroll
@@ -512,9 +512,10 @@ __global__ void __launch_bounds__(kLinThreads)
             }
         cluster_sync();
         if (warp >= 2 && !dead) {
-            // four columns at a time, dealt out to the ranks; all ranks' values are requested at once
+            // four columns at a time, dealt out to the ranks and halves; all ranks'
+            // values are requested at once
             const uint32_t mine = smem_u32(part);
-            for (int c = rank * 4; c < nc; c += p.ks * 4) {
+            for (int c = (rank * 2 + half) * 4; c < nc; c += p.ks * 8) {
                 float q[kMaxKs][4], v[4] = {};
 #pragma unroll
                 for (int r = 0; r < kMaxKs; ++r)
@@ -627,7 +628,7 @@ cudaError_t run_linear(const LinCall& c, LinParams p, cudaStream_t s) {
         auto kern = k_linear_pair<ACT>;
         if ((e = ensure_smem(kern, kPairSmem)) != cudaSuccess) return e;
         const int grid = (int)std::min<long long>(tiles2, pairs) * 2;
-        return launch_k_pair(kern, dim3(grid), dim3(kPairThreads), kPairSmem, s, true, ta, tb, p);
+        return launch_k_pair(kern, dim3(grid), dim3(kLinThreads), kPairSmem, s, true, ta, tb, p);
     }
     p.BN = std::min(128, (p.M + 15) / 16 * 16);
     p.n_wt = (p.N + kF - 1) / kF;

@@ -300,7 +300,7 @@ template <int FMT, int NT>
 MOE_DEV void run_steps_f16(uint32_t w, uint32_t half, uint32_t x4, int s, int n, uint32_t sc0, uint32_t sc1, uint32_t sb, uint32_t sx, uint32_t area,
                            uint32_t (&xb)[NT], uint32_t (&tab)[NT][2], uint32_t tstep, int ntn, float (&acc)[NT][4]) {
     if constexpr (FMT == kNvfp4) {
-#pragma unroll(NT == 1 ? 4 : 2)
+#pragma unroll 2
         for (; n > 0; --n, ++s, sb += 4) {
             const uint32_t a = w + ((s & ~3) << 8) + (((s << 5) & 0x60) ^ x4);
             const uint2 p = lds64(a), q = lds64(a + half);
