@@ -313,9 +313,9 @@ MOE_API moe_status moe_shared_expert_ex(const void* x, const moe_experts_w* Ws, 
  * so picks differ from moe_route's fp32 picks only where two scores are within
  * its rounding; activations are rounded once to bf16; sums are fp32 and in a
  * fixed order for a given set of picks (no atomics), y is rounded once.
- * Workspace: moe_decode_workspace_bytes(d, Is); its first 256 bytes must be
- * zero before the first call and are the library's from then on (a barrier
- * count that carries over from call to call).  Calls that share a workspace
+ * Workspace: moe_decode_workspace_bytes(d, Is), zero-filled before the first
+ * call and the library's from then on (it holds counts that carry over from call
+ * to call).  It may serve any layer whose sizes need no more of it.  Calls that share it
  * must run on one device and not overlap on the GPU.  The launch is cooperative
  * (one CTA per SM, all resident); waits between CTAs are bounded and report
  * device error 2. */

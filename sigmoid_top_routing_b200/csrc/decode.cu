@@ -54,6 +54,7 @@ constexpr int kMaxE = 257;                      // 256 experts and the shared on
 constexpr int kMaxK = 32;
 constexpr int kMaxStages = 16;
 constexpr int kMostCounted = 1 << 17;            // comparisons of a selection by counting
+constexpr int kMaxYRows = 16 * 160;              // rows of y times the CTAs that share them
 constexpr int kMaxParts = 4;                    // parts of a router row
 
 struct WMat {                                   // one weight tensor of the experts
@@ -100,6 +101,13 @@ struct DecodeArgs {
     int stages;                                 // ring slots per group
     StageDims sd, sd2;                          // stages of the up and the down products
     int stage_bytes;
+    // y rows of few columns of work (H < 16 rows for half of the CTAs): ysplit
+    // CTAs share a block of 16 rows, each runs a part of the block's work, and the
+    // last one to finish adds the parts up in order
+    int ysplit;
+    Divisor by_ysplit, by_yworkers;
+    float2* ypart;                              // (ysplit, T, H): sums of the routed and the shared experts
+    int* ydone;                                 // per block: CTAs that wrote theirs; zero between calls
     uint32_t wait_limit;
     int* err;
 };
@@ -110,8 +118,7 @@ struct Layout {                                 // shared memory (byte offsets)
     static constexpr int kMask = 0;                                   // kMaxE words: tokens of an expert
     static constexpr int kList = kMask + (kMaxE + kTok * (kMaxK + 1) + 3) / 4 * 16;   // (behind the masks: keys by rank) active expert ids
     static constexpr int kPick = kList + 1040;                        // [kTok][kMaxK] expert of a pick
-    static constexpr int kWt = kPick + kTok * kMaxK * 4;              // [kTok][kMaxK] routing weight
-    static constexpr int kSlot = kWt + kTok * kMaxK * 4;              // [kTok][256] bytes: pick number of an expert
+    static constexpr int kSlot = kPick + kTok * kMaxK * 4;             // [kTok][256] bytes: pick number of an expert
     static constexpr int kMisc = kSlot + kTok * 256;                  // active count, abort flag; maxima and scales of the token rows
     static constexpr int kBar = kMisc + 16 + 2 * kCw * 4;
     static constexpr int kRed = kBar + 2 * kMaxStages * 8;            // group sums; later y sums per warp
@@ -182,11 +189,22 @@ MOE_DEV double logit_of(const DecodeArgs& a, int t, int e) { return f2_value(log
 // (NaN when a logit is NaN, which makes every score of the row NaN).
 MOE_DEV void softmax_stats64(const DecodeArgs& a, int t, double& m, double& z) {
     const int lane = threadIdx.x & 31;
+    double v[8];
     m = -INFINITY;
     z = 0.0;
-    for (int e = lane; e < a.E; e += 32) m = fmax(m, logit_of(a, t, e));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = lane + 32 * i < a.E ? logit_of(a, t, lane + 32 * i) : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmax(m, v[i]);
     for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int e = lane; e < a.E; e += 32) z += exp(logit_of(a, t, e) - m);
+#pragma unroll 1
+    for (int i = 0; i < (a.E + 31) / 32; ++i) {
+        double w = v[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j)
+            if (j == i) w = v[j];
+        if (lane + 32 * i < a.E) z += exp(w - m);
+    }
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
 }
 MOE_DEV double score64(const DecodeArgs& a, double L, double m, double z) {
@@ -285,7 +303,7 @@ MOE_DEV void select_token(const DecodeArgs& a, int t, bool counted, uint32_t* s_
 }
 
 // Routing weights of one token's picks by one warp, 64-bit, rounded once.
-MOE_DEV void weigh_token(const DecodeArgs& a, int t, const int* pick, float* wt, bool write) {
+MOE_DEV void weigh_token(const DecodeArgs& a, int t, const int* pick) {
     const int lane = threadIdx.x & 31;
     double m = 0.0, z = 1.0, s = 0.0, sum = 0.0;
     if (a.softmax) softmax_stats64(a, t, m, z);
@@ -293,12 +311,8 @@ MOE_DEV void weigh_token(const DecodeArgs& a, int t, const int* pick, float* wt,
     if (lane < a.k) s = score64(a, logit_of(a, t, e), m, z);
     for (int j = 0; j < a.k; ++j) sum += __shfl_sync(0xffffffffu, s, j);   // rank order
     if (lane < a.k) {
-        const float w = (float)(a.no_norm ? s * a.scale : s / (sum + (double)a.eps) * a.scale);
-        wt[lane] = w;
-        if (write) {
-            a.idx[(size_t)t * a.k + lane] = e;
-            a.w[(size_t)t * a.k + lane] = w;
-        }
+        a.idx[(size_t)t * a.k + lane] = e;
+        __stcg(a.w + (size_t)t * a.k + lane, (float)(a.no_norm ? s * a.scale : s / (sum + (double)a.eps) * a.scale));
     }
 }
 
@@ -404,7 +418,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
     uint32_t* s_mask = reinterpret_cast<uint32_t*>(sm + L::kMask);
     int* s_list = reinterpret_cast<int*>(sm + L::kList);
     int* s_pick = reinterpret_cast<int*>(sm + L::kPick);
-    float* s_wt = reinterpret_cast<float*>(sm + L::kWt);
     unsigned char* s_slot = sm + L::kSlot;
     int* s_nact = reinterpret_cast<int*>(sm + L::kMisc);
     uint32_t* s_wmax = reinterpret_cast<uint32_t*>(sm + L::kMisc + 16);              // [kCw]
@@ -442,7 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
     const int wk = cta * kGroups + grp;
     // This CTA's rows of y, in tiles of at most 16; each tile's list of
     // (expert, chunk of k) is dealt out to the groups in equal parts.
-    const int yr0 = part(a.H, cta, a.by_grid), yr1 = part(a.H, cta + 1, a.by_grid);
+    int yr0 = part(a.H, cta, a.by_grid), yr1 = part(a.H, cta + 1, a.by_grid), ypart = 0;
+    if (a.ysplit > 1) {
+        const int block = (int)div_by(cta, a.by_ysplit);
+        ypart = cta - block * a.ysplit;
+        yr0 = min(a.H, block * kRows);
+        yr1 = min(a.H, yr0 + kRows);
+    }
     const int ytiles = max(1, (yr1 - yr0 + kRows - 1) / kRows);
     // phases: 0 the shared expert's features, 1 the routed experts', 2.. tiles of y
     auto rows_of_tile = [&](int tile, int& r0, int& n) {
@@ -468,8 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
             rows_of_tile(phase - 2, r0, nr);
             if (nr == 0) return;                // fewer rows than CTAs
             const int total = nact * a.i_stages + a.is_stages;
-            p = (int)((uint32_t)(total * grp) / kGroups);
-            end = (int)((uint32_t)(total * (grp + 1)) / kGroups);
+            p = part(total, ypart * kGroups + grp, a.by_yworkers);
+            end = part(total, ypart * kGroups + grp + 1, a.by_yworkers);
             li = min((int)div_by(p, a.by_i_stages), nact);
             off = p - li * a.i_stages;
         }
@@ -576,9 +595,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
             for (int c = c0; c < c1 && ahead < Sg && ok; ++c, ++ahead) weights(a.sd2, m, u, false, c);
             return ahead < Sg && ok;
         });
-        // the weights of the picks are first needed by the down products
-        for (int t = grp; t < a.T; t += kGroups)
-            weigh_token(a, t, s_pick + t * kMaxK, s_wt + t * kMaxK, cta == 0);
+        // CTA t weighs token t's picks for the grid: 64-bit arithmetic in every CTA
+        // took longer than small layers' products, and the down products, which
+        // need the weights first, are behind the grid barrier anyway
+        if (grp == 0) {
+            if (cta < a.T) weigh_token(a, cta, s_pick + cta * kMaxK);
+            asm volatile("bar.arrive 7, %0;" ::"r"(kCThreads + 32) : "memory");
+        }
         named_bar(6, kThreads);                 // every h is written
         fence_proxy_async_all();
         if (*s_abort) ok = false;
@@ -806,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
             const StageDims& sd = up ? a.sd : a.sd2;
             if (phase == 2) {                   // every h is written
                 fence_proxy_async_all();        // (the down stages read it through the async proxy)
-                named_bar(5, kCThreads);
+                named_bar(7, kCThreads + 32);   // with the producer warp that weighs
                 if (tid == 0) arrive();
                 if (tid == 0) grid_wait();
                 named_bar(6, kThreads);
@@ -833,6 +856,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                     col[n] = (up ? xs + nth_bit(mask, c) * xstride : a.sd2.tokens + c * (a.sd2.k * 2 + F::kXPad)) +
                              t4 * (FMT == kBf16 ? 16 : 32);
                 }
+                float wcol[NT][2] = {};         // down: weights of this lane's result columns (ahead of the wait)
+                if (!up && u.e < a.E)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int c = n * 8 + 2 * t4 + q;
+                            if (c < ncol) {
+                                const int t = nth_bit(mask, c);
+                                wcol[n][q] = __ldcg(a.w + (size_t)t * a.k + s_slot[t * 256 + u.e]);
+                            }
+                        }
                 uint32_t tcol[NT][2] = {};      // affine up: table entries of this lane's result columns
                 if (FMT == kAffine && up)
 #pragma unroll
@@ -931,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                             if (c < ncol) {
                                 const int t = nth_bit(mask, c);
                                 const bool routed = u.e < a.E;
-                                const float w = (routed ? s_wt[t * kMaxK + s_slot[t * 256 + u.e]] : 1.0f) * gl;
+                                const float w = (routed ? wcol[n][i] : 1.0f) * gl;
                                 float* y = routed ? yw : ysw;
                                 y[sg * TT + t] += w * acc[n][i];
                                 y[(sg + 8) * TT + t] += w * acc[n][2 + i];
@@ -945,22 +980,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 int r0, nr;
                 rows_of_tile(phase - 2, r0, nr);
                 named_bar(5, kCThreads);
-                if (tid < kRows * TT) do {
-                    const int r = tid % kRows, t = tid / kRows;
-                    if (r >= nr || t >= a.T || dead) break;
-                    const size_t o = (size_t)t * a.H + r0 + r;
-                    float v = 0.0f;
+                const int r = tid % kRows, t = tid / kRows;
+                const bool mine = tid < kRows * TT && r < nr && t < a.T;
+                const size_t o = (size_t)t * a.H + r0 + r;
+                float v = 0.0f, sh = 0.0f;
+                if (mine) {
 #pragma unroll
                     for (int w = 0; w < kCw; ++w) v += s_red[(w * kRows + r) * TT + t];
-                    v *= a.out_scale;           // once, on the finished sum
-                    if (a.Is > 0) {
-                        float sh = 0.0f;
+                    if (a.Is > 0)
                         for (int w = 0; w < kCw; ++w) sh += s_red[L::kRedBytes / 8 + (w * kRows + r) * TT + t];
-                        v += sh;
+                }
+                bool finish = true;
+                if (a.ysplit > 1 && nr > 0) {
+                    if (mine) __stcg(a.ypart + (size_t)ypart * a.T * a.H + o, make_float2(v, sh));
+                    __threadfence();
+                    named_bar(5, kCThreads);
+                    if (tid == 0) {
+                        const int block = r0 / kRows;
+                        *s_nact = atomicAdd(a.ydone + block, 1);     // (the active count is no longer needed)
+                        if (*s_nact == a.ysplit - 1) a.ydone[block] = 0;
+                        __threadfence();
                     }
+                    named_bar(5, kCThreads);
+                    finish = *s_nact == a.ysplit - 1;
+                    if (finish && mine) {
+                        v = sh = 0.0f;
+                        for (int q = 0; q < a.ysplit; ++q) {
+                            const float2 p = __ldcg(a.ypart + (size_t)q * a.T * a.H + o);
+                            v += p.x;
+                            sh += p.y;
+                        }
+                    }
+                }
+                if (mine && finish && !dead) {
+                    v *= a.out_scale;           // once, on the finished sum
+                    if (a.Is > 0) v += sh;
                     if (a.residual) v += res;
                     a.y[o] = f2bf16(v);
-                } while (0);
+                }
                 named_bar(5, kCThreads);
             }
         }
@@ -971,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
 struct Plan {
     DecodeArgs a;
     uint64_t magic;
-    size_t smem, ws_bytes, ws_lg, ws_h, ws_hs;
+    size_t smem, ws_bytes, ws_lg, ws_h, ws_hs, ws_yp;
     int device, grid;
     cudaError_t (*launch)(const Plan&, const DecodeArgs&, cudaStream_t);
 };
@@ -1046,6 +1103,19 @@ cudaError_t plan(Plan& p) {
     a.by_I = divisor(a.I);
     a.by_E = divisor(a.E);
     a.by_i_stages = divisor(a.i_stages);
+    const int blocks = (a.H + kRows - 1) / kRows;
+    // stages of a tile of y, when every pick goes to an expert of its own
+    const int work = std::min(a.E, a.T * a.k) * a.i_stages + a.is_stages;
+    // Adding the parts up costs ~2.5 us (2 x 128 x 256 x 8 experts, one token: 11.5
+    // -> 14.0 us); a group's stage ~0.7 us (9 tokens, 20 experts of 320 x 1984,
+    // affine: 60.5 -> 43.1 us): split where a group has 6 stages or more, into
+    // parts of at least 2.
+    if (work >= 6 * kGroups)
+        a.ysplit = std::max(1, std::min(std::min(di.sm_count, kMaxYRows / kRows) / blocks, work / (2 * kGroups)));
+    else
+        a.ysplit = 1;
+    a.by_ysplit = divisor(a.ysplit);
+    a.by_yworkers = divisor(a.ysplit * kGroups);
     if ((uint64_t)a.E * a.I * (di.sm_count * kGroups + 1) >> 32) return cudaErrorNotSupported;   // part()
     p.smem = smem;
     p.grid = di.sm_count;
@@ -1062,18 +1132,19 @@ cudaError_t plan_fmt(Plan& p, bool dual) {
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct DecodeWs {
-    size_t lg, h, hs, total;                    // behind 256 bytes of barrier count
+    size_t lg, h, hs, yp, total;                // behind 1 KB of counts
 };
 
 DecodeWs ws_layout(const moe_dims* d, int Is) {
     DecodeWs L{};
-    size_t off = 256;
+    size_t off = 1024;
     L.lg = off;
     off = align256(off + (size_t)kMaxParts * d->T * d->E * 8);
     L.h = off;
     off = align256(off + (size_t)d->T * d->k * d->I * 2);
     L.hs = off;
-    L.total = align256(off + (size_t)d->T * Is * 2);
+    L.yp = off = align256(off + (size_t)d->T * Is * 2);
+    L.total = align256(off + (size_t)d->T * kMaxYRows * 8);
     return L;
 }
 
@@ -1189,6 +1260,7 @@ moe_status moe_decode_prepare(const moe_layer* L, const moe_dims* d, moe_decode_
     p.ws_lg = wl.lg;
     p.ws_h = wl.h;
     p.ws_hs = wl.hs;
+    p.ws_yp = wl.yp;
     p.magic = kPlanMagic;
     cudaError_t e = cudaGetDevice(&p.device);
     if (e == cudaSuccess && d->T > 0)            // an empty batch launches nothing
@@ -1226,6 +1298,8 @@ moe_status moe_decode_run(const moe_decode_plan* plan, const void* x, const floa
     p.a.lg = reinterpret_cast<float2*>(b + p.ws_lg);
     p.a.h = reinterpret_cast<uint16_t*>(b + p.ws_h);
     p.a.hs = reinterpret_cast<uint16_t*>(b + p.ws_hs);
+    p.a.ypart = reinterpret_cast<float2*>(b + p.ws_yp);
+    p.a.ydone = reinterpret_cast<int*>(b + 256);
     if (e == cudaSuccess) e = p.launch(p, p.a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return refuse(MOE_ERR_CUDA, cudaGetErrorString(e));
     set_last_launch_count(1);

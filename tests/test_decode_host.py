@@ -53,7 +53,7 @@ def test_shared_width(lib, Is):
 def test_workspace(lib):
     d = _d(T=16, H=4096, E=256, k=32, I=2048)
     n = lib.moe_decode_workspace_bytes(ctypes.byref(d), 1024)
-    assert n % 256 == 0 and n >= 256 + 16 * 256 * 8 + 16 * 32 * 2048 * 2 + 16 * 1024 * 2
+    assert n % 256 == 0 and n >= 1024 + 16 * 256 * 8 + 16 * 32 * 2048 * 2 + 16 * 1024 * 2
     L = _layer(Ws=_w(), Is=1024)
     assert _call(lib, L, d, n=n - 1) == abi.MOE_ERR_WORKSPACE
     assert _call(lib, L, d, ws=None) == abi.MOE_ERR_WORKSPACE

@@ -59,7 +59,7 @@ def make_layer(api, inp, **over):
               max_tokens=wl.T)
     kw.update(over)
     layer = api.DecodeLayer(D.W, D.w_router, D.expert_bias, **kw)
-    layer.ws[256:].fill_(0xFF)                       # only the counters need zeros
+    layer.ws[1024:].fill_(0xFF)                      # only the counts need zeros
     return D, layer
 
 
@@ -121,7 +121,7 @@ def run_and_compare(api, wl, residual=True, logits=None):
     for b in (yb, ib, wb):
         assert (b[0] == -1).all() and (b[-1] == -1).all()
     G = torch.cuda.get_device_properties(0).multi_processor_count
-    assert int(layer.ws[:8].view(torch.int64)) % G == 0 and (layer.ws[8:256] == 0).all()
+    assert int(layer.ws[:8].view(torch.int64)) % G == 0 and (layer.ws[8:1024] == 0).all()
     compare(inp, bits(y), ib[1:-1].cpu().numpy(), wb.view(torch.float32)[1:-1].cpu().numpy(), res, logits)
 
 
