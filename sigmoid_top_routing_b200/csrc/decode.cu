@@ -101,6 +101,8 @@ struct DecodeArgs {
     int stages;                                 // ring slots per group
     StageDims sd, sd2;                          // stages of the up and the down products
     int stage_bytes;
+    int ys_off;                                 // shared memory of the shared expert's y sums
+    int ring_off;
     // y rows of few columns of work (H < 16 rows for half of the CTAs): ysplit
     // CTAs share a block of 16 rows, each runs a part of the block's work, and the
     // last one to finish adds the parts up in order
@@ -123,11 +125,12 @@ struct Layout {                                 // shared memory (byte offsets)
     static constexpr int kBar = kMisc + 16 + 2 * kCw * 4;
     static constexpr int kRed = kBar + 2 * kMaxStages * 8;            // group sums; later y sums per warp
     static constexpr int kRedBuf = kGw * kRows * kTok * 4;            // one buffer of one group
-    static constexpr int kRedBytes = kGroups * 2 * kRedBuf;
-    static constexpr int kYs = kRed + kRedBytes / 2;                  // the shared expert's y sums per warp
+    static constexpr int kBufs = NT == 1 ? 2 : 1;                     // buffers of a group
+    static constexpr int kRedBytes = kGroups * kBufs * kRedBuf;       // 16 KB
+    static constexpr int kYw = kCw * kRows * kTok * 4;                // one set of y sums per warp
     static constexpr int kX = (kRed + kRedBytes + 127) & ~127;
     static_assert(kTok * 256 * 4 <= kRedBytes, "the score keys fit them too");
-    static_assert(2 * kCw * kRows * kTok * 4 <= kRedBytes, "both y sums fit the group-sum buffers");
+    static_assert((NT == 1 ? 2 : 1) * kYw <= kRedBytes, "y sums (16 columns: the routed experts' only) fit the group-sum buffers");
 };
 
 MOE_DEV uint64_t key64(double c) {              // order of c; NaN lowest (1), -0 == +0
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
     // affine: per group of 64 k and token (constant part of the products, sum of x)
     float2* s_tab = reinterpret_cast<float2*>(sm + L::kX + a.T * xstride);
     const uint32_t tab0 = xs + a.T * xstride;
-    const uint32_t ring = (tab0 + (FMT == kAffine ? a.H / 64 * a.T * 8 : 0) + 1023) & ~1023u;   // swizzled boxes start on 1 KB
+    const uint32_t ring = (smem_u32(sm) + a.ring_off + 1023) & ~1023u;   // swizzled boxes start on 1 KB
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = gridDim.x, cta = blockIdx.x;
@@ -818,10 +821,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         const int nact = *s_nact;
         int slot = 0;                           // this group's next ring slot, and its parity
         uint32_t ph = 0;
-        float* red = s_red + grp * 2 * (L::kRedBuf / 4);
+        float* red = s_red + grp * L::kBufs * (L::kRedBuf / 4);
         int rbuf = 0;
         float* yw = s_red + warp * kRows * TT;                  // this warp's sums [row][token] of a tile of y
-        float* ysw = reinterpret_cast<float*>(sm + L::kYs) + warp * kRows * TT;   // and the shared expert's
+        float* s_ys = reinterpret_cast<float*>(sm + a.ys_off);   // and the shared expert's, of all warps
+        float* ysw = s_ys + warp * kRows * TT;
 
 #pragma unroll 1
         for (int phase = 0; phase < 2 + ytiles; ++phase) {
@@ -837,7 +841,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
             }
             float res = 0.0f;                   // this thread's element of the tile's residual
             if (!up) {
-                for (int i = lane; i < kRows * TT; i += 32) yw[i] = ysw[i] = 0.0f;
+                for (int i = lane; i < kRows * TT; i += 32) {
+                    yw[i] = 0.0f;
+                    if (a.Is > 0) ysw[i] = 0.0f;
+                }
                 __syncwarp();
                 int r0, nr;
                 rows_of_tile(phase - 2, r0, nr);
@@ -924,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 if (up) {
                     // the group's four k shares meet in shared memory
                     float* r = red + rbuf * (L::kRedBuf / 4);
-                    rbuf ^= 1;
+                    if (L::kBufs == 2) rbuf ^= 1;
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         if (n < ntn) {
@@ -957,6 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                         const int pos = u.f0 + f;
                         __stcg(const_cast<uint16_t*>(h_row(u.e, mask, c)) + (FMT == kBf16 ? pos : pair_pos(pos)), f2bf16(v));
                     }
+                    if (L::kBufs == 1) named_bar(1 + grp, kGw * 32);   // the buffer is read
                 } else {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -988,7 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
 #pragma unroll
                     for (int w = 0; w < kCw; ++w) v += s_red[(w * kRows + r) * TT + t];
                     if (a.Is > 0)
-                        for (int w = 0; w < kCw; ++w) sh += s_red[L::kRedBytes / 8 + (w * kRows + r) * TT + t];
+                        for (int w = 0; w < kCw; ++w) sh += s_ys[(w * kRows + r) * TT + t];
                 }
                 bool finish = true;
                 if (a.ysplit > 1 && nr > 0) {
@@ -1056,8 +1064,15 @@ cudaError_t plan(Plan& p) {
     const DeviceInfo& di = device_info();
     using F = Fmt<FMT>;
     // + 1 KB: the ring starts on a multiple of that
-    const size_t fixed =
-        Layout<NT>::kX + (size_t)a.T * (a.H * 2 + F::kXPad + (FMT == kAffine ? a.H / 8 : 0)) + 1024;
+    // token rows and (affine) their table; the shared expert's y sums lie in the
+    // second half of the group-sum buffers, or for 16 columns over the token
+    // rows, which the down products no longer read, where those are long enough
+    using L = Layout<NT>;
+    const int x_bytes = a.T * (a.H * 2 + F::kXPad + (FMT == kAffine ? a.H / 8 : 0));
+    const bool over_x = NT == 2 && x_bytes >= L::kYw;
+    a.ys_off = NT == 1 ? L::kRed + L::kYw : over_x ? L::kX : (L::kX + x_bytes + 15) & ~15;
+    a.ring_off = NT == 1 || over_x ? L::kX + x_bytes : a.ys_off + L::kYw;
+    const size_t fixed = (size_t)a.ring_off + 1024;
     const int room = fixed < (size_t)di.max_smem_optin ? (int)(di.max_smem_optin - fixed) : 0;
     // Two slots per group of 16 KB of weights each where they fit, smaller ones
     // (at last a single one) where the token rows leave less room.  Down stages

@@ -35,7 +35,7 @@ enum { kBf16 = 0, kAffine = 1, kNvfp4 = 2 };          // the library's weight fo
 
 constexpr int kRows = 16;                             // weight rows of a stage (the MMA's M)
 constexpr int kStep = 64;                             // k per step
-constexpr int kSpanMaxK = 4096;                       // 4-bit: longest row whose scales come as one span per half
+constexpr int kSpanMaxK = 2048;                       // 4-bit: longest row whose scales come as one span per half
 
 // Layout of one stage for `chunks` 128-byte chunks of each row.
 struct StageDims {
@@ -62,6 +62,7 @@ struct Fmt {
     // banks (as plain spans, rows of 64 or 128 bytes cost 4 or 8 wavefronts a load).
     static constexpr int kScaleBox = FMT == kAffine ? 64 : 128;
     static bool boxed(int chunks, int K) {
+        if (K == 0) return false;
         return FMT == kNvfp4 ? K % 256 == 0 : FMT == kAffine && K % 512 == 0 && chunks % 2 == 0;
     }
     // Bytes of one scale array of a stage, for rows of length K.
@@ -79,7 +80,8 @@ struct Fmt {
         d.half = chunks * 1024;
         d.scales = 2 * d.half;
         const int a1 = scale_area(chunks, K1), a2 = scale_area(chunks, K2);
-        d.area = ((a1 > a2 ? a1 : a2) + 1023) & ~1023;   // both arrays and halves start on a swizzle period
+d.area = a1 > a2 ? a1 : a2;
+        if (boxed(chunks, K1) || boxed(chunks, K2)) d.area = (d.area + 1023) & ~1023;   // halves start on a swizzle period
         d.tokens = d.scales + (FMT == kAffine ? 2 * d.area : d.area);
         d.bytes = (d.tokens + cols * (d.k * 2 + kXPad) + 1023) & ~1023;
         return d;

@@ -137,14 +137,21 @@ W = G.Workload
     W("wide", T=9, H=2176, E=6, k=2, I=192, shared_I=64),                      # 9 columns; 4-bit rows in 2 chunks
     W("long", T=2, H=192, E=4, k=2, I=4160, act="relu2"),                      # long down rows, odd groups
     W("many", T=16, H=128, E=256, k=32, I=64),                                 # the most experts and picks
+    W("few_rows", T=9, H=320, E=24, k=5, I=704, shared_I=256, out_scale=0.5),  # blocks of y shared by CTAs
+    W("two_blocks", T=16, H=1152, E=40, k=2, I=256, act="relu2"),
     W("softmax", T=13, H=512, E=40, k=5, I=256, score="softmax", norm_topk=False),
 ], ids=lambda w: w.name)
 def test_parity(api, wl, fmt):
     run_and_compare(api, dataclasses.replace(wl, fmt=fmt, name=f"{wl.name}_{fmt}"))
 
 
-def test_limits_of_the_sizes(api):
-    run_and_compare(api, W("t16", T=16, H=4096, E=4, k=2, I=64))               # T * H = 65536
+@pytest.mark.parametrize("fmt", ["bf16", "affine4", "nvfp4"])
+def test_limits_of_the_sizes(api, fmt):
+    run_and_compare(api, W("t16", T=16, H=4096, E=4, k=2, I=64, shared_I=64, fmt=fmt))   # T * H = 65536
+    run_and_compare(api, W("t15", T=15, H=4352, E=3, k=1, I=128, act="relu2", fmt=fmt))
+
+
+def test_longest_rows(api):
     run_and_compare(api, W("h16384", T=4, H=16384, E=3, k=1, I=64), residual=False)
 
 
@@ -166,6 +173,92 @@ def test_ties_take_the_lower_expert(api):
     inp.expert_bias[:] = 0.0
     run_and_compare(api, wl, logits=lg)
     _CACHE.clear()
+
+
+@pytest.mark.parametrize("T,E,k", [(3, 12, 4), (16, 200, 6)])                 # ranked by counting, and by rounds
+def test_close_scores_rank_by_their_64_bit_values(api, T, E, k):
+    """Logits one fp32 step apart: their fp32 sigmoids are equal, their real ones are not."""
+    wl = W("close", T=T, H=64, E=E, k=k, I=64)
+    inp = inputs_of(wl)
+    inp.expert_bias[:] = 0.0
+    lg = np.full((T, E), -3.0, dtype=np.float32)
+    v = np.float32(9.0)
+    for i in range(k + 2):                                                     # the larger, the later its expert
+        lg[:, E - 2 * (k + 2) + 2 * i] = v
+        v = np.nextafter(v, np.float32(20.0))
+    s32 = (1 / (1 + np.exp(-lg[0]))).astype(np.float32)
+    assert len(np.unique(s32)) == 2                                            # one value but for the -3s
+    run_and_compare(api, wl, residual=False, logits=lg)
+    _CACHE.clear()
+
+
+def test_router_sums_survive_cancellation(api):
+    """Expert logits of ~1e-3 apart that are differences of terms of ~1e4: an fp32 sum
+    would not rank them."""
+    wl = W("cancel", T=5, H=512, E=16, k=3, I=64)
+    inp = inputs_of(wl)
+    rng = np.random.default_rng(4)
+    x = O.bf16_to_f64(inp.x_bits)
+    x[:, 256:] = -x[:, :256]                                                   # exact in bf16
+    inp.x_bits[:] = G.f32_to_bf16_bits(x.astype(np.float32))
+    big = (rng.standard_normal((16, 256)) * 1e4).astype(np.float32)
+    small = (rng.standard_normal((16, 256)) * 1e-3).astype(np.float32)
+    inp.w_router[:] = np.concatenate([big + small, big], axis=1)
+    want = x @ inp.w_router.astype(np.float64).T
+    seq = np.zeros((5, 16), dtype=np.float32)
+    for h in range(512):
+        seq += x[:, h:h + 1].astype(np.float32) * inp.w_router[None, :, h]
+    assert np.abs(seq - want).max() > 1e-3                                     # what one fp32 chain would give
+    run_and_compare(api, wl)
+    _CACHE.clear()
+
+
+def test_one_shot_c_call(api):
+    """moe_decode is moe_decode_prepare and moe_decode_run in one."""
+    import ctypes
+
+    from sigmoid_top_routing_b200 import abi
+    wl = W("oneshot", T=6, H=256, E=8, k=2, I=128, shared_I=64)
+    D, layer = make_layer(api, inputs_of(wl))
+    want, idx, w = layer(D.x)
+    y, i2, w2 = torch.empty_like(want), torch.empty_like(idx), torch.empty_like(w)
+    d = abi.moe_dims(wl.T, wl.H, wl.E, wl.k, wl.I)
+    st = abi.load().moe_decode(ctypes.byref(layer._layer), ctypes.byref(d), D.x.data_ptr(), None, None, i2.data_ptr(),
+                               w2.data_ptr(), y.data_ptr(), layer.ws.data_ptr(), layer.ws.numel(),
+                               torch.cuda.current_stream().cuda_stream)
+    assert st == abi.MOE_OK
+    assert torch.equal(y, want) and torch.equal(i2, idx) and torch.equal(w2, w)
+
+
+def test_layers_share_a_workspace_in_turn(api):
+    """Layers of other sizes may take turns on one zeroed workspace."""
+    a = make_layer(api, G.make_inputs(W("ws_a", T=9, H=320, E=24, k=5, I=704)))
+    b = make_layer(api, G.make_inputs(W("ws_b", T=2, H=256, E=8, k=2, I=128, fmt="nvfp4")))
+    want = [[t.clone() for t in layer(D.x)] for D, layer in (a, b)]
+    ws = torch.zeros(max(a[1].ws.numel(), b[1].ws.numel()), dtype=torch.uint8, device="cuda")
+    a[1].ws = b[1].ws = ws
+    for _ in range(3):
+        for (D, layer), ref in zip((a, b), want):
+            for t, r in zip(layer(D.x), ref):
+                assert torch.equal(t, r)
+
+
+def test_calls_on_two_streams_of_two_layers(api):
+    """Layers of their own may be called at once."""
+    made = [make_layer(api, G.make_inputs(W(f"par{i}", T=4, H=512, E=16, k=4, I=256, seed=i))) for i in range(2)]
+    want = [[t.clone() for t in layer(D.x)] for D, layer in made]
+    streams = [torch.cuda.Stream() for _ in made]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (D, layer) in enumerate(made):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(layer(D.x, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            for t, r in zip(out, want[i]):
+                assert torch.equal(t, r)
 
 
 def test_nan_and_infinite_rows(api):
