@@ -399,16 +399,16 @@ MOE_DEV void issue_weights(const StageDims& sd, const WMat& m, const Unit& u, bo
     }
 }
 
-// Stage address of the scales of row `loc` of a half at stage c (its first byte,
-// before the swizzle's term).
+// Where the scales of row `loc` of a half (first row: `base`) start at stage c,
+// from the stage's scale area on (before the swizzle's term).
 template <int FMT>
-MOE_DEV uint32_t scale_addr(const StageDims& sd, const WMat& m, const Unit& u, int half, int loc, int c, uint32_t st) {
+MOE_DEV uint32_t scale_off(int area, int stage_k, int K, bool boxed, uint32_t base, int half, int loc, int c) {
     using F = Fmt<FMT>;
-    if (m.boxed) return st + sd.scales + half * (sd.area / 2) + loc * F::kScaleBox;
+    if (boxed) return half * (area / 2) + loc * F::kScaleBox;
     // only the low 4 bits of the global byte count: 32-bit products do
-    const uint32_t base = half ? u.row1 : u.row0, SB = (uint32_t)F::scale_bytes(m.K), o = (uint32_t)F::scale_bytes(c * sd.k);
-    if (m.K <= kSpanMaxK) return st + sd.scales + half * (sd.area / 2) + ((base * SB) & 15) + loc * SB + o;
-    return st + sd.scales + (half * 8 + loc) * (sd.area / kRows) + (((base + loc) * SB + o) & 15);
+    const uint32_t SB = (uint32_t)F::scale_bytes(K), o = (uint32_t)F::scale_bytes(c * stage_k);
+    if (K <= kSpanMaxK) return half * (area / 2) + ((base * SB) & 15) + loc * SB + o;
+    return (half * 8 + loc) * (area / kRows) + (((base + loc) * SB + o) & 15);
 }
 
 template <int FMT, int NT, bool DUAL>
@@ -473,8 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         n = (ytiles == 1 ? rows : rows * (tile + 1) / ytiles) - r0;
         r0 += yr0;
     };
-    // Calls f(unit, weights, first chunk, end chunk) for the group's units of a
-    // phase, in order; f returns false to stop.  A down unit is a run of chunks
+    // Calls f(unit, of a routed expert, first stage, end stage) for the group's units
+    // of a phase, in order; f returns false to stop.  A down unit is a run of chunks
     // of one expert: a tile's (expert, chunk) list is dealt out to the groups.
     auto walk = [&](int phase, int nact, auto&& f) {
         int p, end, li = 0, off = 0, r0 = 0, nr = 0;
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 c0 = off;
                 c1 = off + took;
             }
-            if (!f(u, phase < 2 ? (routed ? a.W1 : a.S1) : (routed ? a.W2 : a.S2), c0, c1)) return;
+            if (!f(u, routed, c0, c1)) return;
             p += took;
             off += took;
             if (off == width) {
@@ -572,30 +572,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         };
         // the shared expert's first rows need no routing: fill the free slots with them
         int pre = 0;
-        walk(0, 0, [&](const Unit& u, const WMat& m, int c0, int c1) {
+        if (a.Is > 0) walk(0, 0, [&](const Unit& u, bool, int c0, int c1) {
             for (int c = c0; c < c1 && pre < Sg; ++c, ++pre) {
-                weights(a.sd, m, u, DUAL, c);
+                weights(a.sd, a.S1, u, DUAL, c);
                 no_tokens();
             }
             return pre < Sg;
         });
         __syncthreads();                        // routing tables ready
         const int nact = *s_nact;
-        for (int phase = 0; phase < 2; ++phase) {
-            int q = phase ? pre : 0;
-            walk(phase, nact, [&](const Unit& u, const WMat& m, int c0, int c1) {
+        if (a.Is > 0) {
+            int q = 0;
+            walk(0, nact, [&](const Unit& u, bool, int c0, int c1) {
                 for (int c = c0; c < c1 && ok; ++c)
                     if (q++ >= pre) {
-                        weights(a.sd, m, u, DUAL, c);
+                        weights(a.sd, a.S1, u, DUAL, c);
                         if (ok) no_tokens();
                     }
                 return ok;
             });
         }
+        walk(1, nact, [&](const Unit& u, bool, int c0, int c1) {
+            for (int c = c0; c < c1 && ok; ++c) {
+                weights(a.sd, a.W1, u, DUAL, c);
+                if (ok) no_tokens();
+            }
+            return ok;
+        });
         // Down: the first Sg stages' weights are requested before h is there.
         int ahead = 0;
-        walk(2, nact, [&](const Unit& u, const WMat& m, int c0, int c1) {
-            for (int c = c0; c < c1 && ahead < Sg && ok; ++c, ++ahead) weights(a.sd2, m, u, false, c);
+        walk(2, nact, [&](const Unit& u, bool routed, int c0, int c1) {
+            for (int c = c0; c < c1 && ahead < Sg && ok; ++c, ++ahead) weights(a.sd2, routed ? a.W2 : a.S2, u, false, c);
             return ahead < Sg && ok;
         });
         // CTA t weighs token t's picks for the grid: 64-bit arithmetic in every CTA
@@ -610,10 +617,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         if (*s_abort) ok = false;
         for (int tile = 0; tile < ytiles; ++tile) {
             int q = tile ? ahead : 0;
-            walk(2 + tile, nact, [&](const Unit& u, const WMat& m, int c0, int c1) {
+            walk(2 + tile, nact, [&](const Unit& u, bool routed, int c0, int c1) {
                 for (int c = c0; c < c1 && ok; ++c) {
-                    if (q++ >= ahead) weights(a.sd2, m, u, false, c);
-                    if (ok) tokens(u, m.K, c);
+                    if (q++ >= ahead) weights(a.sd2, routed ? a.W2 : a.S2, u, false, c);
+                    if (ok) tokens(u, routed ? a.I : a.Is, c);
                 }
                 return ok;
             });
@@ -828,9 +835,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         float* ysw = s_ys + warp * kRows * TT;
 
 #pragma unroll 1
-        for (int phase = 0; phase < 2 + ytiles; ++phase) {
+        for (int phase = a.Is > 0 ? 0 : 1; phase < 2 + ytiles; ++phase) {
             const bool up = phase < 2;
-            const StageDims& sd = up ? a.sd : a.sd2;
+            // (selected one by one: through a reference every use would be an indexed
+            // constant load, ~50 cycles each in a row)
+            const int sd_k = up ? a.sd.k : a.sd2.k, sd_half = up ? a.sd.half : a.sd2.half;
+            const int sd_area = up ? a.sd.area : a.sd2.area, sd_scales = up ? a.sd.scales : a.sd2.scales;
             if (phase == 2) {                   // every h is written
                 fence_proxy_async_all();        // (the down stages read it through the async proxy)
                 named_bar(7, kCThreads + 32);   // with the producer warp that weighs
@@ -851,7 +861,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 const int r = tid % kRows, t = tid / kRows;
                 if (a.residual && r < nr && t < a.T) res = bf16f(a.residual[(size_t)t * a.H + r0 + r]);
             }
-            walk(phase, nact, [&](const Unit& u, const WMat& m, int c0, int c1) {
+            walk(phase, nact, [&](const Unit& u, bool routed, int c0, int c1) {
+                const int K = up ? a.H : routed ? a.I : a.Is;
+                const bool boxed = FMT != kBf16 && (up ? a.W1.boxed : routed ? a.W2.boxed : a.S2.boxed);
                 const uint32_t mask = s_mask[u.e];
                 const int ncol = __popc(mask), ntn = (ncol + 7) / 8;
                 float acc[NT][4];
@@ -885,17 +897,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                             tcol[n][q] = tab0 + nth_bit(mask, c < ncol ? c : 0) * 8;
                         }
                 for (int c = c0; c < c1; ++c) {
-                    const int s = ring0 + slot, steps = min(sd.k, m.K - c * sd.k) / kStep;
+                    const int s = ring0 + slot, steps = min(sd_k, K - c * sd_k) / kStep;
                     const uint32_t st = ring + s * a.stage_bytes;
                     const int s0 = (uint32_t)(steps * gw) / kGw, n = (uint32_t)(steps * (gw + 1)) / kGw - s0;
                     uint32_t xb[NT], sc0 = 0, sc1 = 0, sb = 0, sx = 0;
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) xb[i] = col[i] + (up ? c * sd.k * 2 : st) + s0 * (kStep * 2);
+                    for (int i = 0; i < NT; ++i) xb[i] = col[i] + (up ? c * sd_k * 2 : st) + s0 * (kStep * 2);
                     if (FMT != kBf16) {
                         sb = s0 * (FMT == kAffine ? 2 : 4) + (FMT == kNvfp4 ? t4 : 0);
-                        sx = !m.boxed ? 0 : FMT == kNvfp4 ? sg << 4 : (sg >> 1) << 4;
-                        sc0 = scale_addr<FMT>(sd, m, u, 0, sg, c, st);
-                        sc1 = scale_addr<FMT>(sd, m, u, 1, sg, c, st);
+                        sx = !boxed ? 0 : FMT == kNvfp4 ? sg << 4 : (sg >> 1) << 4;
+                        sc0 = st + sd_scales + scale_off<FMT>(sd_area, sd_k, K, boxed, u.row0, 0, sg, c);
+                        sc1 = st + sd_scales + scale_off<FMT>(sd_area, sd_k, K, boxed, u.row1, 1, sg, c);
                     }
                     if (!dead) {
                         const bool got = mbar_wait(&full[s], ph, s_abort, a.wait_limit);
@@ -912,11 +924,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
 #pragma unroll
                                 for (int i = 0; i < NT; ++i)
 #pragma unroll
-                                    for (int q = 0; q < 2; ++q) tab[i][q] = tcol[i][q] + (c * (sd.k / 64) + s0) * a.T * 8;
-                            run_steps_f16<FMT, NT>(st + sg * 128, sd.half, x4, s0, n, sc0, sc1, sb, sx, sd.area, xb, tab, a.T * 8,
+                                    for (int q = 0; q < 2; ++q) tab[i][q] = tcol[i][q] + (c * (sd_k / 64) + s0) * a.T * 8;
+                            run_steps_f16<FMT, NT>(st + sg * 128, sd_half, x4, s0, n, sc0, sc1, sb, sx, sd_area, xb, tab, a.T * 8,
                                                    ntn, acc);
                         } else {
-                            run_steps<FMT, NT>(st + sg * 128, sd.half, x4, s0, n, sc0, sc1, sb, sx, sd.area, xb, ntn, acc);
+                            run_steps<FMT, NT>(st + sg * 128, sd_half, x4, s0, n, sc0, sc1, sb, sx, sd_area, xb, ntn, acc);
                         }
                     }
                     __syncwarp();
@@ -927,7 +939,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                     }
                 }
                 // NVFP4: the expert's global scale (bf16 products carry 2^-8)
-                const float gl = FMT == kNvfp4 ? (up ? 1.0f : 256.0f) * __ldg(m.glob + (u.e == a.E ? 0 : u.e)) : 1.0f;
+                const float gl = FMT == kNvfp4 ? (up ? 1.0f : 256.0f) * __ldg((up ? (routed ? a.W1.glob : a.S1.glob) : (routed ? a.W2.glob : a.S2.glob)) +
+                                                                              (routed ? u.e : 0))
+                                               : 1.0f;
                 if (up) {
                     // the group's four k shares meet in shared memory
                     float* r = red + rbuf * (L::kRedBuf / 4);
@@ -956,7 +970,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                         }
                         if (DUAL) {
                             clamp_swiglu(v, w, u.e == a.E ? a.limit_s : a.limit);
-                            v = act_swiglu(v, w);
+                            // (fast exp and quotient, ~2^-19: the result is rounded to bf16)
+                            v = __fdividef(v, 1.0f + __expf(-v)) * w;
                         } else {
                             v = act_relu2(v);
                         }
@@ -973,7 +988,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                             const int c = n * 8 + 2 * t4 + i;
                             if (c < ncol) {
                                 const int t = nth_bit(mask, c);
-                                const bool routed = u.e < a.E;
                                 const float w = (routed ? wcol[n][i] : 1.0f) * gl;
                                 float* y = routed ? yw : ysw;
                                 y[sg * TT + t] += w * acc[n][i];
