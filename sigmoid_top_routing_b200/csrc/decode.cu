@@ -7,30 +7,43 @@
 //   y = bf16(out_scale * sum_j w_j W2[e_j] h_j + W2s act(W1s x) + residual)
 //
 // At this size the layer is one pass over the picked experts' weights, so the
-// kernel is built around that stream.  One CTA per SM; a producer warp copies
-// weight rows into a ring of stages with bulk copies and 16 consumer warps, in
-// 4 groups of 4, multiply them with the token rows on m16n8k16 MMAs (the token
-// count is at most the MMA's N, so the tensor cores idle either way; see
-// stream.cuh for the stage layout).
+// kernel is built around that stream.  One CTA per SM, 16 consumer warps in 4
+// groups of 4 and a producer warp per group.  A group has its own part of the
+// work and its own slots of a shared-memory ring, which its producer fills by TMA
+// (stream.cuh has the stage layout); its 4 warps share a tile's k and multiply
+// with m16n8k16 MMAs -- the token count is at most the MMA's N, so tensor
+// throughput does not matter; reading and converting weights does.  One producer
+// for all groups measured 192 us where four take 82 (8 tokens, bf16, below).
 //
 //   up    The active experts' features (I per routed expert) form one list;
-//         every CTA takes an equal contiguous part of it, in tiles of 8
+//         every group takes an equal contiguous part of it, in tiles of 8
 //         features (SwiGLU: 8 gate and 8 up rows, which meet in one thread) or
 //         16 (relu^2).  h goes to global memory, one row per routed pair.
 //   down  Every CTA owns H / CTAs rows of y and runs them through all active
 //         experts, so y needs no atomics and no second pass: partial sums
-//         stay in shared memory and one fixed-order sum ends the row.
+//         stay in shared memory and one fixed-order sum ends the row.  With few
+//         rows and many experts, CTAs share blocks of 16 rows instead and the
+//         last one of a block adds its parts up, in order.
 //
 // Two grid barriers (after the logits, after h) join the phases; the launch is
 // cooperative, so all CTAs are resident and the waits end.  Neither stops the
-// stream of weights for long: the producer fetches the shared expert's rows
-// before the routing is known and the down rows before h is.
+// stream of weights for long: the producers fetch the shared expert's rows
+// before the routing is known and the first down rows before h is.  (Consumers
+// that do not wait at the second barrier, and logits polled by tags instead of
+// the first, both measured slower: more fences and more polls on one line.)
 //
 // Router sums carry ~46 bits (fp32 pairs) and close scores are compared in 64: E * H * T
 // is small here, and picks are then those of the real-number scores up to ties.
 //
-// Bound: HBM for bf16 experts from a few tokens on; latency (barriers, first
-// loads, launch) at one token.
+// Measured (device time of a call, weights rotated through more than L2; floor =
+// bytes at 6455 GB/s): 16 tokens, 32 experts, k = 4, 2048 x 1792, bf16: 93-97 us
+// (floor 96 by the expected number of active experts); 8 tokens 82 us (72); one token of relu^2 64 experts, k = 6, 2048 x 1024
+// with a shared expert 24 us (10.5); 4-bit 64 experts, k = 4, 2048 x 1536: one
+// affine token 21-22 us (3.4), five NVFP4 tokens 45 us (15); one token of a tiny
+// block 11 us.  Bound: HBM for bf16 from a few tokens on; the conversion of codes
+// (integer instructions at half rate) and the per-tile work for 4 bits; for one
+// token ~11 us of latency, a chain of a launch, two fenced grid barriers (~1.5 us
+// each), three dependent memory round trips and the selection.
 #include <algorithm>
 #include <cstring>
 
@@ -103,9 +116,8 @@ struct DecodeArgs {
     int stage_bytes;
     int ys_off;                                 // shared memory of the shared expert's y sums
     int ring_off;
-    // y rows of few columns of work (H < 16 rows for half of the CTAs): ysplit
-    // CTAs share a block of 16 rows, each runs a part of the block's work, and the
-    // last one to finish adds the parts up in order
+    // > 1 (few rows of y, much work for each): ysplit CTAs share a block of 16 rows,
+    // each runs a part of its work, and the last one to finish adds the parts up
     int ysplit;
     Divisor by_ysplit, by_yworkers;
     float2* ypart;                              // (ysplit, T, H): sums of the routed and the shared experts
