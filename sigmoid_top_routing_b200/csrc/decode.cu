@@ -39,7 +39,7 @@
 // bytes at 6455 GB/s): 16 tokens, 32 experts, k = 4, 2048 x 1792, bf16: 93-97 us
 // (floor 96 by the expected number of active experts); 8 tokens 82 us (72); one token of relu^2 64 experts, k = 6, 2048 x 1024
 // with a shared expert 24 us (10.5); 4-bit 64 experts, k = 4, 2048 x 1536: one
-// affine token 21-22 us (3.4), five NVFP4 tokens 45 us (15); one token of a tiny
+// affine token 21 us (3.4), five NVFP4 tokens 45 us (15); one token of a tiny
 // block 11 us.  Bound: HBM for bf16 from a few tokens on; the conversion of codes
 // (integer instructions at half rate) and the per-tile work for 4 bits; for one
 // token ~11 us of latency, a chain of a launch, two fenced grid barriers (~1.5 us
