@@ -306,7 +306,8 @@ MOE_API moe_status moe_shared_expert_ex(const void* x, const moe_experts_w* Ws, 
  *               moe_shared_expert, with W's fmt and act), scalars.
  *   x           bf16 (T, H).  Routing reads x, or logits (fp32 (T, E)) when given.
  *   residual    bf16 (T, H) or NULL, added to the finished sum in fp32.
- *   topk_idx, topk_w, y   outputs as of moe_forward_ex.  y may be residual or x.
+ *   topk_idx, topk_w, y   outputs as of moe_forward_ex.  y may be residual or x
+ *               (a residual that y overlaps in part is MOE_ERR_UNSUPPORTED).
  * Sizes: moe_dims' limits, T <= MOE_DECODE_MAX_T and T * H <= 65536
  * (MOE_ERR_SHAPE otherwise: moe_forward takes those).
  * Arithmetic: logits, scores and weights in 64-bit (topk_w rounded once to fp32),
@@ -318,7 +319,7 @@ MOE_API moe_status moe_shared_expert_ex(const void* x, const moe_experts_w* Ws, 
  * to call).  It may serve any layer whose sizes need no more of it.  Calls that share it
  * must run on one device and not overlap on the GPU.  The launch is cooperative
  * (one CTA per SM, all resident); waits between CTAs are bounded and report
- * device error 2. */
+ * device error 2 (zero-fill the workspace again after it). */
 #define MOE_DECODE_MAX_T 16
 typedef struct {
     const float* w_router;
@@ -361,7 +362,8 @@ MOE_API moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void*
  *   residual  bf16 or (res_f32 = 1) fp32 (M, N), row stride ldr, or NULL; added
  *             after the activation
  *   y         bf16 or (y_f32 = 1) fp32 (M, N), row stride ldy.  y may be residual
- *             (same pointer, type and stride); it must not overlap x or w.
+ *             (same pointer, type and stride); any other overlap with an input
+ *             is MOE_ERR_UNSUPPORTED (column blocks of one buffer do not overlap).
  * Row strides are in elements, 0 = dense.  x and w are 16-byte aligned with
  * strides that are multiples of 8 elements (MOE_ERR_ALIGN); residual and y only
  * to their element, with any stride >= N.  0 <= M, 1 <= N, 1 <= K, each up to 2^24.

@@ -264,7 +264,7 @@ def moe_linear(x, w, bias=None, residual=None, *, act: str = "none", swiglu_limi
     last with w = [gate; up] of 2N rows).  x (M, K) and w are bf16 with row strides
     that are multiples of 8; bias is fp32; residual and y are bf16 or fp32 with any
     row stride.  y defaults to a new bf16 (or ``out_dtype``) tensor; it may be the
-    residual itself."""
+    residual itself, any other overlap with an input is refused."""
     if not x.is_cuda or x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w: expected CUDA matrices")
     dev, (M, K), rows = x.device, x.shape, w.shape[0]

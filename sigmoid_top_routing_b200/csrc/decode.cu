@@ -1241,7 +1241,7 @@ moe_status check_layer(const moe_layer* L, const moe_dims* d) {
 // What a call brings.
 moe_status check_call(const void* x, const float* logits, const float* w_router, const void* residual,
                       const int32_t* topk_idx, const float* topk_w, const void* y, const void* ws, size_t ws_bytes,
-                      size_t need) {
+                      size_t need, size_t row_bytes) {
     if (!x || !y) return refuse(MOE_ERR_NULL, "x or y is NULL");
     if (!topk_idx || !topk_w) return refuse(MOE_ERR_NULL, "topk_idx or topk_w is NULL");
     if (!logits && !w_router) return refuse(MOE_ERR_NULL, "w_router is NULL (routing from x)");
@@ -1249,6 +1249,10 @@ moe_status check_call(const void* x, const float* logits, const float* w_router,
     if (misaligned(residual, 16)) return refuse(MOE_ERR_ALIGN, "residual not 16-byte aligned");
     if (misaligned(logits, 4) || misaligned(topk_idx, 4) || misaligned(topk_w, 4))
         return refuse(MOE_ERR_ALIGN, "logits, topk_idx or topk_w not 4-byte aligned");
+    // (x may lie anywhere in y: every CTA has its copy before the first store to y)
+    const uintptr_t py = reinterpret_cast<uintptr_t>(y), pr = reinterpret_cast<uintptr_t>(residual);
+    if (residual && pr != py && pr < py + row_bytes && py < pr + row_bytes)
+        return refuse(MOE_ERR_UNSUPPORTED, "moe_decode: y overlaps a part of residual (it may be residual itself)");
     if (!ws) return refuse(MOE_ERR_WORKSPACE, "workspace is NULL");
     if (misaligned(ws, 256)) return refuse(MOE_ERR_ALIGN, "workspace not 256-byte aligned");
     if (ws_bytes < need) return refuse(MOE_ERR_WORKSPACE, "workspace smaller than moe_decode_workspace_bytes()");
@@ -1322,7 +1326,8 @@ moe_status moe_decode_run(const moe_decode_plan* plan, const void* x, const floa
     memcpy(&p, plan, sizeof p);
     if (p.magic != kPlanMagic) return refuse(MOE_ERR_UNSUPPORTED, "not a plan of moe_decode_prepare");
     if (p.a.T == 0) return set_last_launch_count(0), MOE_OK;   // empty batch: nothing to do
-    const moe_status st = check_call(x, logits, p.a.w_router, residual, topk_idx, topk_w, y, ws, ws_bytes, p.ws_bytes);
+    const moe_status st = check_call(x, logits, p.a.w_router, residual, topk_idx, topk_w, y, ws, ws_bytes, p.ws_bytes,
+                                     (size_t)p.a.T * p.a.H * 2);
     if (st != MOE_OK) return st;
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1353,7 +1358,8 @@ moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void* x, cons
     moe_status st = check_layer(L, d);
     if (st != MOE_OK) return st;
     if (d->T == 0) return set_last_launch_count(0), MOE_OK;   // empty batch: nothing to do
-    st = check_call(x, logits, L->w_router, residual, topk_idx, topk_w, y, ws, ws_bytes, ws_layout(d, L->Is).total);
+    st = check_call(x, logits, L->w_router, residual, topk_idx, topk_w, y, ws, ws_bytes, ws_layout(d, L->Is).total,
+                    (size_t)d->T * d->H * 2);
     if (st != MOE_OK) return st;
     moe_decode_plan plan;
     st = moe_decode_prepare(L, d, &plan);

@@ -674,6 +674,26 @@ moe_status refuse(moe_status st, const char* msg) {
 }
 bool misaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
+// A matrix in memory, in bytes.
+struct Span {
+    uintptr_t p;
+    long long rows, row, pitch;
+    Span(const void* q, long long rows, long long cols, long long ld, int es)
+        : p(reinterpret_cast<uintptr_t>(q)), rows(rows), row(cols * es), pitch(rows > 1 ? ld * es : cols * es) {}
+    uintptr_t end() const { return p + (uintptr_t)((rows - 1) * pitch + row); }
+};
+// Whether two of them share a byte.  Column blocks of one buffer (same pitch) do
+// not; rows that interleave with another pitch count as shared.
+bool overlap(const Span& a, const Span& b) {
+    if (a.p >= b.end() || b.p >= a.end()) return false;
+    const Span &lo = a.p <= b.p ? a : b, &hi = a.p <= b.p ? b : a;
+    if (lo.rows > 1 && hi.rows > 1 && lo.pitch != hi.pitch) return true;
+    if (lo.rows == 1 && hi.rows == 1) return true;
+    const long long pitch = std::max(lo.rows > 1 ? lo.pitch : 0, hi.rows > 1 ? hi.pitch : 0);
+    const long long off = (long long)(hi.p - lo.p) % pitch;
+    return off < lo.row || off + hi.row > pitch;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -702,6 +722,15 @@ extern "C" moe_status moe_linear(const void* x, const void* w, const float* bias
     if (misaligned(x, 16) || misaligned(w, 16)) return refuse(MOE_ERR_ALIGN, "x or w not 16-byte aligned");
     if (misaligned(bias, 4) || misaligned(residual, cfg->res_f32 ? 4 : 2) || misaligned(y, cfg->y_f32 ? 4 : 2))
         return refuse(MOE_ERR_ALIGN, "bias, residual or y not aligned to its elements");
+    // y is written while other tiles still read x and w; a residual element is read
+    // by the thread that writes its place in y, and by no other
+    const Span sy(y, d->M, d->N, ldy, cfg->y_f32 ? 4 : 2);
+    const long long rows = (cfg->act == MOE_ACT_SWIGLU ? 2ll : 1ll) * d->N;
+    const bool in_place = residual == y && cfg->res_f32 == cfg->y_f32 && (ldr == ldy || d->M == 1);
+    if (overlap(sy, Span(x, d->M, d->K, ldx, 2)) || overlap(sy, Span(w, rows, d->K, ldw, 2)) ||
+        (bias && overlap(sy, Span(bias, 1, rows, rows, 4))) ||
+        (residual && !in_place && overlap(sy, Span(residual, d->M, d->N, ldr, cfg->res_f32 ? 4 : 2))))
+        return refuse(MOE_ERR_UNSUPPORTED, "moe_linear: y overlaps an input (only the residual itself may be y)");
     LinCall c{x, w, ldx, ldw, d->K};
     LinParams p{};
     p.bias = bias;

@@ -65,6 +65,7 @@ def test_workspace(lib):
     (dict(w=None), abi.MOE_ERR_NULL), (dict(x=0x10008), abi.MOE_ERR_ALIGN), (dict(y=0x40002), abi.MOE_ERR_ALIGN),
     (dict(residual=0x60008), abi.MOE_ERR_ALIGN), (dict(logits=0x60002), abi.MOE_ERR_ALIGN),
     (dict(idx=0x20002), abi.MOE_ERR_ALIGN),
+    (dict(residual=0x40200), abi.MOE_ERR_UNSUPPORTED), (dict(residual=0x40000 - 2032), abi.MOE_ERR_UNSUPPORTED),
 ])
 def test_pointers(lib, over, status):
     assert _call(lib, **over) == status

@@ -138,6 +138,21 @@ def test_residual_in_place(api, M, dtype):
     assert got.data_ptr() == r.data_ptr() and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("M", [1, 6, 700])
+def test_column_blocks_of_one_buffer(api, M):
+    """x, the residual and y side by side in the rows of one buffer."""
+    x, w, b, r = make(M, 64, 256, bias=True, residual=torch.bfloat16)
+    buf = torch.full((M, 400), float("nan"), dtype=torch.bfloat16, device="cuda")
+    buf[:, :256], buf[:, 264:328] = x, r
+    check(api, buf[:, :256], w, b, buf[:, 264:328], y=buf[:, 328:392])
+    assert torch.equal(buf[:, :256], x) and torch.equal(buf[:, 264:328], r)
+    assert buf[:, 256:264].isnan().all() and buf[:, 392:].isnan().all()
+    with pytest.raises(RuntimeError, match="overlaps"):
+        api.moe_linear(buf[:, :256], w, b, y=buf[:, 192:256])
+    with pytest.raises(RuntimeError, match="overlaps"):
+        api.moe_linear(x, w, b, buf[:, 328:392], y=buf[:, 330:394])
+
+
 @pytest.mark.parametrize("M", [4, 512])
 def test_clamp_and_special_values(api, M):
     x, w, b, r = make(M, 600, 128, "swiglu", bias=True, seed=5)

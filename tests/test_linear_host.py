@@ -40,6 +40,21 @@ def test_refusals(lib, bad, status):
     assert _call(lib, **bad) == status
 
 
+# M = 4, N = 32, K = 64 at their dense strides: x is 512 bytes, w 4096, bias 128, y 256
+@pytest.mark.parametrize("bad", [
+    dict(y=0x10000), dict(y=0x101fe), dict(y=0x10000 - 254), dict(y=0x20000 + 4094), dict(act=0, y=0x20000 + 8190),
+    dict(bias=0x30000), dict(bias=0x30000 - 124), dict(act=0, bias=0x30000 - 252),
+    dict(residual=0x30040), dict(residual=0x30000, res_f32=1), dict(residual=0x30000, ldr=40),
+    dict(x=0x10000, ldx=128, y=0x1007e, ldy=128),                    # column blocks that share column 63
+    dict(x=0x10000, ldx=128, y=0x10080 + 66, ldy=128),               # a block that runs into the next row of x
+    dict(x=0x10000, ldx=128, y=0x10080, ldy=64),                     # interleaved with another stride
+    dict(M=1, x=0x10000, y=0x10010),
+    dict(M=1, y=0x20000 + 128 * 5),                                  # a single row of y in w
+])
+def test_outputs_over_inputs(lib, bad):
+    assert _call(lib, **bad) == abi.MOE_ERR_UNSUPPORTED
+
+
 def test_null_structs_and_empty_batch(lib):
     c = abi.moe_linear_cfg(2, 0, 0, 0.0)
     assert lib.moe_linear(0x10000, 0x20000, None, None, None, ctypes.byref(c), 0x30000, None) == abi.MOE_ERR_NULL
