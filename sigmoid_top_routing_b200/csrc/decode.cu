@@ -988,6 +988,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                             v = act_relu2(v);
                         }
                         // the activation is rounded once to bf16, the down products' operand type
+                        // and moe_experts' h.  Its rounding adds to y's own: y is off by 0.0020-
+                        // 0.0025 of its size (rms) instead of 0.0016.  h as a sum of two bf16
+                        // took that away for 5 NVFP4 tokens 45 -> 48 us, 8 bf16 tokens 82 -> 88,
+                        // 16 tokens 93 -> 115 (token rows crowd the weights out of the ring)
                         const int pos = u.f0 + f;
                         __stcg(const_cast<uint16_t*>(h_row(u.e, mask, c)) + (FMT == kBf16 ? pos : pair_pos(pos)), f2bf16(v));
                     }
