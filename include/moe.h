@@ -346,6 +346,30 @@ MOE_API moe_status moe_decode_run(const moe_decode_plan* plan, const void* x, co
                                   const void* residual, int32_t* topk_idx, float* topk_w, void* y, void* ws,
                                   size_t ws_bytes, moe_stream_t stream);
 MOE_API size_t moe_decode_workspace_bytes(const moe_dims* d, int32_t Is);
+/* Shared memory of moe_decode's CTAs for these sizes and a device whose CTAs may
+ * have smem_bytes of it (for inspection and tests: no device is needed).  Offsets
+ * are in bytes.  A ring slot holds one stage of the up (w1) or the down products
+ * (w2): two halves of 8 weight rows of `half` bytes, then the scales (4-bit), then
+ * the tokens' activations (down).  Scales take `area` bytes (affine: as much again
+ * behind them for the biases) and lie in one of three ways, by the row length K:
+ *   boxed         a TMA box per half at area / 2: 8 rows of 128 bytes (NVFP4) or 64
+ *                 (affine), swizzled with a period of 1024 or 512 bytes
+ *   K <= 2048     the span of a half's 8 scale rows, from the 16-byte unit it starts in, at area / 2
+ *   else          each of the 16 rows' span at multiples of area / 16
+ * One stage of the down products serves w2 (K = I) and the shared w2 (K = Is). */
+typedef struct {
+    int32_t chunks, k;                 /* 128-byte chunks, and k, of a row in one stage */
+    int32_t half, scales, area, tokens, bytes;
+} moe_decode_stage;
+typedef struct {
+    int64_t smem;                      /* dynamic shared memory of a CTA; 0: not one stage fits */
+    int32_t ring;                      /* where the ring starts, rounded up to 1024 */
+    int32_t slots, stage_bytes;        /* of each of the 4 groups */
+    int32_t boxed_up, boxed_down, boxed_shared;
+    moe_decode_stage up, down;
+} moe_decode_smem;
+MOE_API moe_status moe_decode_smem_layout(const moe_dims* d, int32_t Is, int32_t fmt, int32_t smem_bytes,
+                                          moe_decode_smem* out);
 MOE_API moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void* x, const float* logits,
                               const void* residual, int32_t* topk_idx, float* topk_w, void* y, void* ws,
                               size_t ws_bytes, moe_stream_t stream);

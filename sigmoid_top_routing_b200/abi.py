@@ -66,6 +66,16 @@ class moe_decode_plan(ctypes.Structure):
     _fields_ = [("opaque", ctypes.c_uint64 * 384)]
 
 
+class moe_decode_stage(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("chunks", "k", "half", "scales", "area", "tokens", "bytes")]
+
+
+class moe_decode_smem(ctypes.Structure):
+    _fields_ = [("smem", c_int64), ("ring", c_int32), ("slots", c_int32), ("stage_bytes", c_int32),
+                ("boxed_up", c_int32), ("boxed_down", c_int32), ("boxed_shared", c_int32),
+                ("up", moe_decode_stage), ("down", moe_decode_stage)]
+
+
 class moe_linear_dims(ctypes.Structure):
     _fields_ = [("M", c_int32), ("N", c_int32), ("K", c_int32),
                 ("ldx", c_int64), ("ldw", c_int64), ("ldr", c_int64), ("ldy", c_int64)]
@@ -106,6 +116,7 @@ PROTOTYPES = {
     "moe_linear": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, POINTER(moe_linear_dims), POINTER(moe_linear_cfg),
                              c_void_p, c_void_p]),
     "moe_decode_workspace_bytes": (c_size_t, [POINTER(moe_dims), c_int32]),
+    "moe_decode_smem_layout": (c_int32, [POINTER(moe_dims), c_int32, c_int32, c_int32, POINTER(moe_decode_smem)]),
     "moe_decode_prepare": (c_int32, [POINTER(moe_layer), POINTER(moe_dims), POINTER(moe_decode_plan)]),
     "moe_decode_run": (c_int32, [POINTER(moe_decode_plan), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                  c_void_p, c_size_t, c_void_p]),

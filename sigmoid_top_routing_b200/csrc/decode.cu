@@ -46,6 +46,7 @@
 // each), three dependent memory round trips and the selection.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -1088,10 +1089,10 @@ cudaError_t launch(const Plan& p, const DecodeArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k_decode<FMT, NT, DUAL>, a);
 }
 
-template <int FMT, int NT, bool DUAL>
-cudaError_t plan(Plan& p) {
-    DecodeArgs& a = p.a;
-    const DeviceInfo& di = device_info();
+// Shared memory of a CTA that may have max_smem bytes: the ring's stages and what
+// lies in front of it.  The bytes to ask for, or 0 where not one stage fits.
+template <int FMT, int NT>
+size_t lay_out(DecodeArgs& a, int max_smem) {
     using F = Fmt<FMT>;
     // + 1 KB: the ring starts on a multiple of that
     // token rows and (affine) their table; the shared expert's y sums lie in the
@@ -1103,7 +1104,7 @@ cudaError_t plan(Plan& p) {
     a.ys_off = NT == 1 ? L::kRed + L::kYw : over_x ? L::kX : (L::kX + x_bytes + 15) & ~15;
     a.ring_off = NT == 1 || over_x ? L::kX + x_bytes : a.ys_off + L::kYw;
     const size_t fixed = (size_t)a.ring_off + 1024;
-    const int room = fixed < (size_t)di.max_smem_optin ? (int)(di.max_smem_optin - fixed) : 0;
+    const int room = fixed < (size_t)max_smem ? (int)(max_smem - fixed) : 0;
     // Two slots per group of 16 KB of weights each where they fit, smaller ones
     // (at last a single one) where the token rows leave less room.  Down stages
     // hold the columns' activations too: as many chunks as fit behind them.
@@ -1120,8 +1121,17 @@ cudaError_t plan(Plan& p) {
     a.sd2 = down(c2);
     a.stage_bytes = std::max(a.sd.bytes, a.sd2.bytes);
     a.stages = std::min(kMaxStages, room / a.stage_bytes) / kGroups;
-    if (a.stages < 1) return cudaErrorNotSupported;
-    const size_t smem = fixed + (size_t)kGroups * a.stages * a.stage_bytes;
+    return a.stages < 1 ? 0 : fixed + (size_t)kGroups * a.stages * a.stage_bytes;
+}
+
+template <int FMT, int NT, bool DUAL>
+cudaError_t plan(Plan& p) {
+    DecodeArgs& a = p.a;
+    const DeviceInfo& di = device_info();
+    using F = Fmt<FMT>;
+    const size_t smem = lay_out<FMT, NT>(a, di.max_smem_optin);
+    if (!smem) return cudaErrorNotSupported;
+    const int c1 = a.sd.chunks, c2 = a.sd2.chunks;
     const int n1 = a.E * a.W1.rows, n2 = a.E * a.W2.rows;
     auto map = [&](WMat& m, int rows, int chunks) {
         const uint64_t bytes = FMT == kBf16 ? (uint64_t)m.K * 2 : (uint64_t)m.K / 2;
@@ -1272,6 +1282,38 @@ extern "C" {
 
 size_t moe_decode_workspace_bytes(const moe_dims* d, int32_t Is) {
     return check_sizes(d, Is) == MOE_OK ? ws_layout(d, Is).total : 0;
+}
+
+moe_status moe_decode_smem_layout(const moe_dims* d, int32_t Is, int32_t fmt, int32_t smem_bytes, moe_decode_smem* out) {
+    const moe_status st = check_sizes(d, Is);
+    if (st != MOE_OK) return st;
+    if (!out) return refuse(MOE_ERR_NULL, "out is NULL");
+    if (fmt != MOE_W_BF16 && fmt != MOE_W_AFFINE4_G64 && fmt != MOE_W_NVFP4) return refuse(MOE_ERR_UNSUPPORTED, "fmt");
+    if (d->T == 0) return refuse(MOE_ERR_SHAPE, "moe_decode_smem_layout: T = 0 launches nothing");
+    DecodeArgs a{};
+    a.T = d->T;
+    a.H = d->H;
+    a.I = d->I;
+    a.Is = Is;
+    const auto go = [&](auto f) {
+        constexpr int F = decltype(f)::value;
+        out->smem = (int64_t)(d->T <= 8 ? lay_out<F, 1>(a, smem_bytes) : lay_out<F, 2>(a, smem_bytes));
+        out->boxed_up = Fmt<F>::boxed(a.sd.chunks, a.H);
+        out->boxed_down = Fmt<F>::boxed(a.sd2.chunks, a.I);
+        out->boxed_shared = Fmt<F>::boxed(a.sd2.chunks, Is);
+    };
+    if (fmt == MOE_W_BF16) go(std::integral_constant<int, kBf16>());
+    else if (fmt == MOE_W_AFFINE4_G64) go(std::integral_constant<int, kAffine>());
+    else go(std::integral_constant<int, kNvfp4>());
+    out->ring = a.ring_off;
+    out->slots = a.stages;
+    out->stage_bytes = a.stage_bytes;
+    const auto stage = [](const StageDims& s) {
+        return moe_decode_stage{s.chunks, s.k, s.half, s.scales, s.area, s.tokens, s.bytes};
+    };
+    out->up = stage(a.sd);
+    out->down = stage(a.sd2);
+    return MOE_OK;
 }
 
 moe_status moe_decode_prepare(const moe_layer* L, const moe_dims* d, moe_decode_plan* out) {

@@ -65,6 +65,8 @@ struct Fmt {
         if (K == 0) return false;
         return FMT == kNvfp4 ? K % 256 == 0 : FMT == kAffine && K % 512 == 0 && chunks % 2 == 0;
     }
+    // Long unboxed rows: the scales of each of the 16 rows in a slot of its own.
+    static bool row_slots(int chunks, int K) { return FMT != kBf16 && K > kSpanMaxK && !boxed(chunks, K); }
     // Bytes of one scale array of a stage, for rows of length K.
     static int scale_area(int chunks, int K) {
         if (FMT == kBf16 || K == 0) return 0;
@@ -80,7 +82,9 @@ struct Fmt {
         d.half = chunks * 1024;
         d.scales = 2 * d.half;
         const int a1 = scale_area(chunks, K1), a2 = scale_area(chunks, K2);
-d.area = a1 > a2 ? a1 : a2;
+        d.area = a1 > a2 ? a1 : a2;
+        // the larger area may be the other matrix's: 16 row slots still start on 16 bytes
+        if (row_slots(chunks, K1) || row_slots(chunks, K2)) d.area = (d.area + 255) & ~255;
         if (boxed(chunks, K1) || boxed(chunks, K2)) d.area = (d.area + 1023) & ~1023;   // halves start on a swizzle period
         d.tokens = d.scales + (FMT == kAffine ? 2 * d.area : d.area);
         d.bytes = (d.tokens + cols * (d.k * 2 + kXPad) + 1023) & ~1023;

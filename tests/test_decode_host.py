@@ -107,3 +107,79 @@ def test_python_layer_refuses_cpu_tensors_and_shapes():
                           w2=torch.zeros(4, 64, 64, dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         api.DecodeLayer(W, torch.zeros(4, 64), E=4, k=2, I=64)
+
+
+# ---- shared-memory layout of the weight ring ----------------------------------
+SMEM = 232448                                          # 227 KB, the most a CTA of the device may have
+ROWS = [64, 192, 256, 320, 512, 704, 1024, 1472, 1856, 1984, 2048, 2112, 2240, 2304, 2560, 2688, 3008, 3712, 4096,
+        4160, 7168, 8128, 8192, 16320, 16384]
+HIDDEN = [64, 320, 2048, 2176, 2688, 4096, 16384]
+
+
+def _layouts(lib, fmt):
+    """(layout, T, H, I, Is) of every combination of the sizes above that is allowed."""
+    for T in range(1, 17):
+        for H in HIDDEN:
+            if T * H > 65536:
+                continue
+            for I in ROWS:
+                for Is in [0] + ROWS:
+                    m, d = abi.moe_decode_smem(), _d(T=T, H=H, I=I)
+                    assert lib.moe_decode_smem_layout(ctypes.byref(d), Is, fmt, SMEM, ctypes.byref(m)) == abi.MOE_OK
+                    if m.smem:
+                        yield m, T, H, I, Is
+
+
+def _scales_of(fmt, K):
+    """Bytes of one scale array of K weights."""
+    return K // 32 if fmt == abi.MOE_W_AFFINE4_G64 else K // 16
+
+
+def _copies(fmt, st, K, boxed):
+    """(offset from the array's start, most bytes) of the scale copies of a stage of rows of K."""
+    if boxed:
+        return [(h * (st.area // 2), 8 * (64 if fmt == abi.MOE_W_AFFINE4_G64 else 128)) for h in range(2)]
+    if K <= 2048:                                      # 8 rows' span, widened to 16-byte units
+        return [(h * (st.area // 2), (8 * _scales_of(fmt, K) + 30) // 16 * 16) for h in range(2)]
+    return [(r * st.area / 16, (_scales_of(fmt, min(st.k, K)) + 30) // 16 * 16) for r in range(16)]
+
+
+def _check_stage(m, fmt, st, rows, tokens, where):
+    """Every copy of a stage starts on 16 bytes, has room, and touches no other."""
+    arrays = 0 if fmt == abi.MOE_W_BF16 else 2 if fmt == abi.MOE_W_AFFINE4_G64 else 1
+    assert st.scales == 2 * st.half == 2048 * st.chunks, where
+    assert st.tokens == st.scales + arrays * st.area and st.tokens % 16 == 0, where
+    pad = 64 if fmt == abi.MOE_W_BF16 else 16
+    assert st.tokens + tokens * (2 * st.k + pad) <= st.bytes <= m.stage_bytes, where
+    for K, boxed in rows:
+        for a in range(arrays):
+            copies = _copies(fmt, st, K, boxed)
+            ends = [o for o, _ in copies[1:]] + [st.area]
+            for (o, n), end in zip(copies, ends):
+                assert o == int(o) and (st.scales + a * st.area + int(o)) % 16 == 0, (where, K, o)
+                assert o + n <= end, (where, K, o, n, end)
+
+
+@pytest.mark.parametrize("fmt", [abi.MOE_W_BF16, abi.MOE_W_AFFINE4_G64, abi.MOE_W_NVFP4])
+def test_every_copy_of_a_stage_is_aligned_and_inside(lib, fmt):
+    seen = 0
+    for m, T, H, I, Is in _layouts(lib, fmt):
+        where = (T, H, I, Is)
+        assert m.stage_bytes % 1024 == 0 and m.slots >= 1, where
+        assert (m.ring + 1023) // 1024 * 1024 + 4 * m.slots * m.stage_bytes <= m.smem <= SMEM, where
+        _check_stage(m, fmt, m.up, [(H, m.boxed_up)], 0, where)
+        down = [(I, m.boxed_down)] + ([(Is, m.boxed_shared)] if Is else [])
+        _check_stage(m, fmt, m.down, down, T, where)
+        seen += 1
+    assert seen > 50000
+
+
+def test_layout_refusals(lib):
+    m = abi.moe_decode_smem()
+    call = lib.moe_decode_smem_layout
+    assert call(ctypes.byref(_d(T=17)), 0, 0, SMEM, ctypes.byref(m)) == abi.MOE_ERR_SHAPE
+    assert call(ctypes.byref(_d(T=0)), 0, 0, SMEM, ctypes.byref(m)) == abi.MOE_ERR_SHAPE
+    assert call(ctypes.byref(_d()), 32, 0, SMEM, ctypes.byref(m)) == abi.MOE_ERR_SHAPE
+    assert call(ctypes.byref(_d()), 0, 3, SMEM, ctypes.byref(m)) == abi.MOE_ERR_UNSUPPORTED
+    assert call(ctypes.byref(_d()), 0, 0, SMEM, None) == abi.MOE_ERR_NULL
+    assert call(ctypes.byref(_d()), 0, 0, 1024, ctypes.byref(m)) == abi.MOE_OK and m.smem == 0

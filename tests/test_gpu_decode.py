@@ -365,3 +365,18 @@ def test_python_refusals(api):
         api.DecodeLayer(D.W, D.w_router, D.expert_bias, E=4, k=2, I=128)
     with pytest.raises(ValueError):
         api.DecodeLayer(D.W, D.w_router, D.expert_bias, E=4, k=2, I=64, max_tokens=17)
+
+
+# A down stage serves w2 and the shared w2; their scale rows lie differently when one
+# of I, Is is above 2048 and the other is not.  Without a residual, so that the norm
+# gate sees what the experts add.
+@pytest.mark.parametrize("fmt", ["affine4", "nvfp4"])
+@pytest.mark.parametrize("wl", [
+    W("wide_shared_t4", T=4, H=2688, E=6, k=3, I=1856, act="relu2", shared_I=3712),
+    W("wide_shared_t16", T=16, H=2688, E=6, k=3, I=1856, act="relu2", shared_I=3712, out_scale=2.5),
+    W("wide_shared_t10", T=10, H=320, E=8, k=2, I=1984, shared_I=2112),
+    W("wide_experts_t7", T=7, H=448, E=5, k=2, I=2240, shared_I=1472),
+    W("wide_experts_t15", T=15, H=4096, E=3, k=1, I=4160, shared_I=64, act="relu2"),
+], ids=lambda w: w.name)
+def test_shared_width_across_2048(api, wl, fmt):
+    run_and_compare(api, dataclasses.replace(wl, fmt=fmt, name=f"{wl.name}_{fmt}"), residual=False)
