@@ -85,7 +85,8 @@ struct Fmt {
         d.area = a1 > a2 ? a1 : a2;
         // the larger area may be the other matrix's: 16 row slots still start on 16 bytes
         if (row_slots(chunks, K1) || row_slots(chunks, K2)) d.area = (d.area + 255) & ~255;
-        if (boxed(chunks, K1) || boxed(chunks, K2)) d.area = (d.area + 1023) & ~1023;   // halves start on a swizzle period
+        // both halves' boxes (area / 2 apart) start on a swizzle period, 8 box rows
+        if (boxed(chunks, K1) || boxed(chunks, K2)) d.area = (d.area + 16 * kScaleBox - 1) & ~(16 * kScaleBox - 1);
         d.tokens = d.scales + (FMT == kAffine ? 2 * d.area : d.area);
         d.bytes = (d.tokens + cols * (d.k * 2 + kXPad) + 1023) & ~1023;
         return d;

@@ -183,3 +183,17 @@ def test_layout_refusals(lib):
     assert call(ctypes.byref(_d()), 0, 3, SMEM, ctypes.byref(m)) == abi.MOE_ERR_UNSUPPORTED
     assert call(ctypes.byref(_d()), 0, 0, SMEM, None) == abi.MOE_ERR_NULL
     assert call(ctypes.byref(_d()), 0, 0, 1024, ctypes.byref(m)) == abi.MOE_OK and m.smem == 0
+
+
+@pytest.mark.parametrize("fmt,period", [(abi.MOE_W_AFFINE4_G64, 512), (abi.MOE_W_NVFP4, 1024)])
+def test_boxed_scales_start_on_their_swizzle_period(lib, fmt, period):
+    """TMA swizzles by address bits: a box off its period has its rows' 16-byte units elsewhere."""
+    boxes = 0
+    for m, T, H, I, Is in _layouts(lib, fmt):
+        for st, boxed in ((m.up, m.boxed_up), (m.down, m.boxed_down or m.boxed_shared)):
+            if boxed:
+                arrays = 2 if fmt == abi.MOE_W_AFFINE4_G64 else 1
+                starts = [st.scales + a * st.area + h * (st.area // 2) for a in range(arrays) for h in range(2)]
+                assert all(s % period == 0 for s in starts), (T, H, I, Is, st.scales, st.area)
+                boxes += 1
+    assert boxes > 50000

@@ -380,3 +380,16 @@ def test_python_refusals(api):
 ], ids=lambda w: w.name)
 def test_shared_width_across_2048(api, wl, fmt):
     run_and_compare(api, dataclasses.replace(wl, fmt=fmt, name=f"{wl.name}_{fmt}"), residual=False)
+
+
+# NVFP4: one of the two scale arrays in swizzled boxes, the other in row slots, in the
+# same stage; y in blocks of more than 8 rows, whose second half reads the second box.
+@pytest.mark.parametrize("wl", [
+    W("box_i_t1", T=1, H=2048, E=4, k=2, I=2048, shared_I=2112),
+    W("box_is_t1", T=1, H=2176, E=4, k=2, I=2112, shared_I=256, act="relu2"),
+    W("box_i_t2", T=2, H=256, E=6, k=3, I=1536, shared_I=3008),
+    W("box_is_t2", T=2, H=2048, E=4, k=2, I=2240, shared_I=2048, out_scale=0.5),
+    W("box_long_t5", T=5, H=2432, E=3, k=2, I=4096, shared_I=2496, act="relu2"),
+], ids=lambda w: w.name)
+def test_boxed_and_slotted_scales_in_one_stage(api, wl):
+    run_and_compare(api, dataclasses.replace(wl, fmt="nvfp4"), residual=False)
