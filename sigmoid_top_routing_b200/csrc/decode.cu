@@ -227,8 +227,8 @@ MOE_DEV double score64(const DecodeArgs& a, double L, double m, double z) {
     return a.softmax ? (z == z ? exp(L - m) / z : z) : sigmoid64(L);
 }
 
-// Turns a token's logits into score keys (softmax), by one warp.
-MOE_DEV void softmax_keys(const DecodeArgs& a, uint32_t* s_key) {
+// Turns a token's logits into score keys (softmax), by one warp; returns the largest logit.
+MOE_DEV float softmax_keys(const DecodeArgs& a, uint32_t* s_key) {
     const int lane = threadIdx.x & 31;
     float m = -INFINITY, z = 0.0f;
     for (int e = lane; e < a.E; e += 32) m = fmaxf(m, __uint_as_float(s_key[e]));
@@ -239,17 +239,20 @@ MOE_DEV void softmax_keys(const DecodeArgs& a, uint32_t* s_key) {
         const float s = z == z ? expf(__uint_as_float(s_key[e]) - m) / z : z;
         s_key[e] = key32(s + (a.ebias ? __ldg(a.ebias + e) : 0.0f));
     }
+    return m;
 }
 
 // Picks of one token by one warp, from fp32 score keys: already ranked (counted)
 // or by k + 1 rounds of a warp-wide maximum.  The fp32 scores are within 2e-6
 // (1 + |c|) of the 64-bit ones, so where the first k + 1 of them are further
 // apart than twice that, their order is the 64-bit order; else the token is
-// ranked again from 64-bit scores.
+// ranked again from 64-bit scores.  `slack` is added to that distance: a softmax
+// score also moves by up to 2 p (1 - p) |m| 2^-24 <= |m| 2^-25 through the rounding of
+// computed logits to fp32 (m: the largest; far smaller logits have p = 0).
 // (A round is ~500 cycles of latency, the count of a whole rank ~300 for 64
 // experts but E^2 T work: it is used up to kMostCounted comparisons.)
-MOE_DEV void select_token(const DecodeArgs& a, int t, bool counted, uint32_t* s_key, const uint32_t* s_sorted, int* pick,
-                          unsigned char* slot, uint32_t* mask) {
+MOE_DEV void select_token(const DecodeArgs& a, int t, bool counted, float slack, uint32_t* s_key,
+                          const uint32_t* s_sorted, int* pick, unsigned char* slot, uint32_t* mask) {
     const int lane = threadIdx.x & 31;
     int my_e = 0;
     bool close = false;
@@ -259,7 +262,7 @@ MOE_DEV void select_token(const DecodeArgs& a, int t, bool counted, uint32_t* s_
         for (int j = lane; j + 1 < rounds; j += 32) {
             const uint32_t hi = s_sorted[j], lo = s_sorted[j + 1];
             const float c = unkey32(hi);
-            close |= hi > 1u && lo > 1u && !(c - unkey32(lo) > 4e-6f * (1.0f + fabsf(c)));   // both numbers
+            close |= hi > 1u && lo > 1u && !(c - unkey32(lo) > 4e-6f * (1.0f + fabsf(c)) + slack);   // both numbers
         }
         close = __any_sync(0xffffffffu, close);
     } else {
@@ -277,7 +280,7 @@ MOE_DEV void select_token(const DecodeArgs& a, int t, bool counted, uint32_t* s_
             if (lane == j) my_e = e;
             if (j > 0 && last > 1u && top > 1u) {
                 const float c = unkey32(last);
-                close |= !(c - unkey32(top) > 4e-6f * (1.0f + fabsf(c)));
+                close |= !(c - unkey32(top) > 4e-6f * (1.0f + fabsf(c)) + slack);
             }
             last = top;
         }
@@ -791,8 +794,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                 for (int q = a.E; q < Ep; ++q) s_key[tt * Ep + q] = 0u;
         }
         named_bar(5, kCThreads);
+        float slack = 0.0f;
         if (a.softmax) {
-            if (warp < a.T) softmax_keys(a, s_key + warp * Ep);
+            if (warp < a.T) {
+                const float m = softmax_keys(a, s_key + warp * Ep);
+                if (!a.logits) slack = fabsf(m) * 0x1p-23f;      // two scores' share, doubled
+            }
             named_bar(5, kCThreads);
         }
         uint32_t* s_sorted = s_mask + kMaxE;                           // [T][kMaxK + 1]: keys by rank
@@ -816,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
             named_bar(5, kCThreads);
         }
         if (warp < a.T)
-            select_token(a, warp, counted, s_key + warp * Ep, s_sorted + warp * (kMaxK + 1), s_pick + warp * kMaxK,
+            select_token(a, warp, counted, slack, s_key + warp * Ep, s_sorted + warp * (kMaxK + 1), s_pick + warp * kMaxK,
                          s_slot + warp * 256, s_mask);
         named_bar(5, kCThreads);
         if (warp * 32 < a.E) {                  // the active experts, ascending: a warp per 32

@@ -393,3 +393,39 @@ def test_shared_width_across_2048(api, wl, fmt):
 ], ids=lambda w: w.name)
 def test_boxed_and_slotted_scales_in_one_stage(api, wl):
     run_and_compare(api, dataclasses.replace(wl, fmt="nvfp4"), residual=False)
+
+
+@pytest.mark.parametrize("E", [16, 200])                                       # ranked by counting, and by rounds
+def test_softmax_ranks_large_logits_by_their_64_bit_values(api, E):
+    """Router logits of tens of thousands: rounded to fp32 they move a softmax score by
+    5e-5, far past the distance at which two fp32 scores count as close.  The expert bias
+    sets the scores 4e-5 apart; the tokens share them and differ in a common shift of
+    their logits."""
+    T, k, n = 16, 5, 12                                                        # n experts in the running
+    wl = W("soft_large", T=T, H=256, E=E, k=k, I=64, score="softmax")
+    inp = inputs_of(wl)
+    rng = np.random.default_rng(0)
+    x = np.repeat(O.bf16_to_f64(inp.x_bits)[:1], T, axis=0)
+    x[:, 0] = 200 + 2 * np.arange(T)
+    inp.x_bits[:] = G.f32_to_bf16_bits(x.astype(np.float32))
+    inp.w_router[:, 1:] *= 1.5
+    inp.w_router[:, 0] = 125.0
+    runners = rng.permutation(E)[:n]
+    out = np.setdiff1d(np.arange(E), runners)
+    inp.w_router[out, 0] = 123.0                                               # 64 and more behind: a score of ~0
+    L = O.bf16_to_f64(inp.x_bits) @ inp.w_router.astype(np.float64).T
+
+    def softmax(v):
+        p = np.exp(v - v.max(axis=1, keepdims=True))
+        return p / p.sum(axis=1, keepdims=True)
+    p = softmax(L)
+    inp.expert_bias[:] = -1.0
+    inp.expert_bias[runners] = (0.3 - p[0, runners] + 4e-5 * rng.permutation(n)).astype(np.float32)
+    want = np.argsort(-(p + inp.expert_bias), axis=1)[:, :k]
+    r = softmax(L.astype(np.float32).astype(np.float64)) + inp.expert_bias     # scores of rounded logits
+    order = np.argsort(-r, axis=1)[:, :k + 1]
+    c = np.take_along_axis(r, order, axis=1)
+    far = (c[:, :-1] - c[:, 1:] > 4e-6 * (1 + c[:, :-1])).all(axis=1)
+    assert (far & (order[:, :k] != want).any(axis=1)).sum() >= 4               # wrong, and no two of them close
+    run_and_compare(api, wl, residual=False)
+    _CACHE.clear()
