@@ -346,7 +346,8 @@ class DecodeLayer:
     returns ``(y, topk_idx, topk_w)``.  The workspace is the layer's own: its
     calls must not overlap on the GPU (calls on several streams, or graphs that
     replay at once, each need a layer of their own).  The tensors given here are
-    kept, not copied: new values in them count from the next call on.
+    kept, not copied: new values in them count from the next call on, other tensors
+    set as fields of ``W`` or ``Ws`` do not.
     """
 
     def __init__(self, W: ExpertWeights, w_router=None, expert_bias=None, *, E: int, k: int, I: int,
@@ -364,7 +365,8 @@ class DecodeLayer:
         _check_weights("W", W, E, I, self.H, dev)
         if Ws is not None:
             _check_weights("Ws", Ws, 1, Is, self.H, dev)
-        self._keep = (W, Ws, w_router, expert_bias)
+        # the tensors themselves: W's and Ws' fields may be set to others later
+        self._keep = (dataclasses.replace(W), Ws and dataclasses.replace(Ws), w_router, expert_bias)
         self.max_tokens = max_tokens
         d = abi.moe_dims(max_tokens, self.H, E, k, I)
         n = moe_decode_workspace_bytes(d, Is)

@@ -429,3 +429,35 @@ def test_softmax_ranks_large_logits_by_their_64_bit_values(api, E):
     assert (far & (order[:, :k] != want).any(axis=1)).sum() >= 4               # wrong, and no two of them close
     run_and_compare(api, wl, residual=False)
     _CACHE.clear()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "affine4", "nvfp4"])
+def test_layer_keeps_the_tensors_it_was_given(api, fmt):
+    """Fields of the weights set to other tensors, and the router dropped, after the layer was made."""
+    import gc
+    import weakref
+
+    from sigmoid_top_routing_b200.device_inputs import shared_to_device, to_device
+    wl = W("keep", T=4, H=256, E=8, k=2, I=128, shared_I=64, fmt=fmt)
+    inp = inputs_of(wl)
+    D, Ws = to_device(inp), shared_to_device(inp)
+    layer = api.DecodeLayer(D.W, D.w_router, D.expert_bias, E=wl.E, k=wl.k, I=wl.I, Ws=Ws, Is=wl.shared_I)
+    want = [t.clone() for t in layer(D.x)]
+    refs, shapes = [weakref.ref(D.w_router), weakref.ref(D.expert_bias)], []
+    for w in (D.W, Ws):
+        for f in dataclasses.fields(w):
+            t = getattr(w, f.name)
+            if isinstance(t, torch.Tensor):
+                refs.append(weakref.ref(t))
+                shapes.append((t.shape, t.dtype))
+                setattr(w, f.name, None)
+                del t
+    x = D.x
+    del D, Ws, w
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    junk = [torch.empty(s, dtype=d, device="cuda").view(torch.uint8).fill_(0xFF) for s, d in shapes]
+    for T in (4, 3):                                          # 3: prepared after the change
+        for a, b in zip(layer(x[:T]), want):
+            assert torch.equal(a, b[:T])
+    del junk
