@@ -6,6 +6,7 @@ kernels.  Torch provides device memory and streams.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 from typing import Optional
@@ -49,6 +50,18 @@ def _stream_on(stream, device: int) -> int:
     """_stream for the calls whose host time counts: the device's current stream
     without building a torch.cuda.Stream object (3 us)."""
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _alloc_on(stream, device: torch.device):
+    """Context in which tensors belong to the stream that will write them: the allocator
+    may hand out blocks whose last use on the current stream is still to come."""
+    if stream is None or device.type != "cuda" or _stream(stream) == torch._C._cuda_getCurrentRawStream(device.index):
+        return _NO_CONTEXT
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(_stream(stream), device=device))
 
 
 @dataclasses.dataclass
@@ -145,10 +158,11 @@ def moe_route(x=None, logits=None, w_router=None, expert_bias=None, *, E: int, k
     H = x.shape[1] if x is not None else (w_router.shape[1] if w_router is not None else 64)
     d = abi.moe_dims(T, H, E, k, 64)
     dev = src.device
-    if topk_idx is None:
-        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
-    if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    with _alloc_on(stream, dev):
+        if topk_idx is None:
+            topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        if topk_w is None:
+            topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
     rc = router_cfg(score, norm_topk)
     check(load().moe_route_ex(_ptr(x), _ptr(logits), _ptr(w_router), _ptr(expert_bias), ctypes.byref(d),
                               eps, scale, ctypes.byref(rc), _ptr(topk_idx), _ptr(topk_w), _stream(stream)),
@@ -160,8 +174,9 @@ def moe_plan(topk_idx, *, E: int, H: int = 64, I: int = 64, plan: Optional[Plan]
              stream=None) -> Plan:
     T, k = topk_idx.shape
     d = abi.moe_dims(T, H, E, k, I)
-    plan = plan or new_plan(T, E, k, topk_idx.device)
-    ws = ws if ws is not None else new_workspace(d, device=topk_idx.device)
+    with _alloc_on(stream, topk_idx.device):
+        plan = plan or new_plan(T, E, k, topk_idx.device)
+        ws = ws if ws is not None else new_workspace(d, device=topk_idx.device)
     cp = plan.c_struct()
     check(load().moe_plan(_ptr(topk_idx), ctypes.byref(d), ctypes.byref(cp), _ptr(ws), ws.numel(),
                           _stream(stream)), "moe_plan")
@@ -176,9 +191,10 @@ def moe_experts(x, plan: Plan, topk_w, W: ExpertWeights, *, E: int, I: int, out_
     T, H = x.shape
     k = topk_w.shape[1]
     d = abi.moe_dims(T, H, E, k, I)
-    y = y if y is not None else torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     ex = exec_cfg(dispatch, combine)
-    ws = ws if ws is not None else new_workspace(d, W.fmt, x.device, dispatch=dispatch, combine=combine)
+    with _alloc_on(stream, x.device):
+        y = y if y is not None else torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        ws = ws if ws is not None else new_workspace(d, W.fmt, x.device, dispatch=dispatch, combine=combine)
     cp, cw = plan.c_struct(), W.c_struct()
     check(load().moe_experts_ex(_ptr(x), ctypes.byref(cp), _ptr(topk_w), ctypes.byref(d), ctypes.byref(cw),
                                 _ref(ex), skip, _ptr(y_shared), out_scale, _ptr(y), _ptr(ws), ws.numel(),
@@ -196,12 +212,13 @@ def moe_forward(x, W: ExpertWeights, w_router=None, expert_bias=None, *, E: int,
     T, H = x.shape
     d = abi.moe_dims(T, H, E, k, I)
     dev = x.device
-    topk_idx = topk_idx if topk_idx is not None else torch.empty((T, k), dtype=torch.int32, device=dev)
-    topk_w = topk_w if topk_w is not None else torch.empty((T, k), dtype=torch.float32, device=dev)
-    plan = plan or new_plan(T, E, k, dev)
-    y = y if y is not None else torch.empty((T, H), dtype=torch.bfloat16, device=dev)
     ex = exec_cfg(dispatch, combine)
-    ws = ws if ws is not None else new_workspace(d, W.fmt, dev, dispatch=dispatch, combine=combine)
+    with _alloc_on(stream, dev):
+        topk_idx = topk_idx if topk_idx is not None else torch.empty((T, k), dtype=torch.int32, device=dev)
+        topk_w = topk_w if topk_w is not None else torch.empty((T, k), dtype=torch.float32, device=dev)
+        plan = plan or new_plan(T, E, k, dev)
+        y = y if y is not None else torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        ws = ws if ws is not None else new_workspace(d, W.fmt, dev, dispatch=dispatch, combine=combine)
     cp, cw, rc = plan.c_struct(), W.c_struct(), router_cfg(score, norm_topk)
     check(load().moe_forward_ex(_ptr(x), _ptr(logits), _ptr(w_router), _ptr(expert_bias), ctypes.byref(d), eps,
                                 router_scale, out_scale, ctypes.byref(rc), _ref(ex), _ptr(y_shared),
@@ -216,9 +233,10 @@ def moe_shared_expert(x, Ws: ExpertWeights, *, I: int, y_shared=None, ws=None, s
     """fp32 (T, H) output of the shared expert (one expert, weight 1, on every token)."""
     T, H = x.shape
     d = abi.moe_dims(T, H, 1, 1, I)
-    y_shared = y_shared if y_shared is not None else torch.empty((T, H), dtype=torch.float32, device=x.device)
     ex = exec_cfg(dispatch, combine)
-    ws = ws if ws is not None else new_workspace(d, Ws.fmt, x.device, dispatch=dispatch, combine=combine)
+    with _alloc_on(stream, x.device):
+        y_shared = y_shared if y_shared is not None else torch.empty((T, H), dtype=torch.float32, device=x.device)
+        ws = ws if ws is not None else new_workspace(d, Ws.fmt, x.device, dispatch=dispatch, combine=combine)
     cw = Ws.c_struct()
     check(load().moe_shared_expert_ex(_ptr(x), ctypes.byref(cw), ctypes.byref(d), _ref(ex), _ptr(y_shared),
                                       _ptr(ws), ws.numel(), _stream(stream)), "moe_shared_expert")
@@ -285,7 +303,8 @@ def moe_linear(x, w, bias=None, residual=None, *, act: str = "none", swiglu_limi
         ldr = _rows("residual", residual, M, N, _OUT, dev)
         res_p, res_f32 = residual.data_ptr(), residual.dtype is torch.float32
     if y is None:
-        y = x.new_empty((M, N), dtype=out_dtype)   # (None: x's bf16)
+        with _alloc_on(stream, dev):
+            y = x.new_empty((M, N), dtype=out_dtype)   # (None: x's bf16)
         if y.dtype not in _OUT:
             raise ValueError(f"out_dtype: expected bfloat16 or float32, got {out_dtype}")
         ldy = N
@@ -400,18 +419,19 @@ class DecodeLayer:
         if logits is not None:
             _want("logits", logits, (T, self.E), (torch.float32,), dev)
         _, plan, like_idx, like_w = self._plans.get(T) or self._plan(T)
-        if y is None:
-            y = torch.empty_like(x)
-        else:
+        if y is not None:
             _want("y", y, (T, self.H), (torch.bfloat16,), dev)
-        if topk_idx is None:
-            topk_idx = torch.empty_like(like_idx)
-        else:
+        if topk_idx is not None:
             _want("topk_idx", topk_idx, (T, self.k), (torch.int32,), dev)
-        if topk_w is None:
-            topk_w = torch.empty_like(like_w)
-        else:
+        if topk_w is not None:
             _want("topk_w", topk_w, (T, self.k), (torch.float32,), dev)
+        with _alloc_on(stream, dev):
+            if y is None:
+                y = torch.empty_like(x)
+            if topk_idx is None:
+                topk_idx = torch.empty_like(like_idx)
+            if topk_w is None:
+                topk_w = torch.empty_like(like_w)
         if torch.cuda.current_device() != dev.index:
             with torch.cuda.device(dev):
                 st = self._go(plan, x, logits, residual, topk_idx, topk_w, y, stream)

@@ -1,0 +1,92 @@
+"""Calls with ``stream=`` another stream than the current one: what the wrapper
+allocates belongs to the stream that writes it, so a block that the current stream
+still writes is not handed out.  Every test enqueues, on the current stream, a wait
+and then a write into a block that it frees at once."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+CYCLES = 100_000_000                                   # ~50 ms: longer than any call here
+
+
+@pytest.fixture(scope="module")
+def api():
+    from sigmoid_top_routing_b200 import build
+    build.build(quiet=True)
+    from sigmoid_top_routing_b200 import api as A
+    A.load()
+    return A
+
+
+@pytest.fixture(scope="module")
+def block():
+    """(workload, device inputs) of a small block."""
+    from sigmoid_top_routing_b200 import inputs as G
+    from sigmoid_top_routing_b200.device_inputs import to_device
+    wl = G.Workload("streams", T=8, H=512, E=8, k=2, I=128)
+    return wl, to_device(G.make_inputs(wl))
+
+
+def freed_but_written_later(*shapes):
+    """Blocks of the outputs' sizes that the current stream writes after a while, freed now."""
+    torch.cuda._sleep(CYCLES)
+    for shape, dtype in shapes:
+        for _ in range(4):
+            torch.empty(shape, dtype=dtype, device="cuda").view(torch.uint8).fill_(0x55)
+
+
+def same(got, want):
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_linear(api, raw):
+    x, w = torch.randn(64, 256, device="cuda").bfloat16(), torch.randn(512, 256, device="cuda").bfloat16()
+    want = api.moe_linear(x, w)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed_but_written_later(((64, 512), torch.bfloat16))
+    same([api.moe_linear(x, w, stream=s.cuda_stream if raw else s)], [want])
+
+
+def test_decode_layer(api, block):
+    wl, D = block
+    layer = api.DecodeLayer(D.W, D.w_router, D.expert_bias, E=wl.E, k=wl.k, I=wl.I)
+    want = [t.clone() for t in layer(D.x)]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed_but_written_later(((wl.T, wl.H), torch.bfloat16), ((wl.T, wl.k), torch.int32))
+    same(layer(D.x, stream=s), want)
+
+
+def test_forward_and_its_parts(api, block):
+    wl, D = block
+    kw = dict(E=wl.E, k=wl.k, I=wl.I)
+    want = [t.clone() for t in api.moe_forward(D.x, D.W, D.w_router, D.expert_bias, combine=1, **kw)[:3]]
+    s = torch.cuda.Stream()
+    n = api.moe_workspace_bytes(api.dims(wl.T, wl.H, wl.E, wl.k, wl.I), combine=1)
+    torch.cuda.synchronize()
+    shapes = (((wl.T, wl.H), torch.bfloat16), ((wl.T, wl.k), torch.int32), ((n,), torch.uint8))
+    freed_but_written_later(*shapes)
+    got = api.moe_forward(D.x, D.W, D.w_router, D.expert_bias, combine=1, stream=s, **kw)
+    same(got[:3], want)
+    freed_but_written_later(*shapes)
+    idx, w = api.moe_route(D.x, None, D.w_router, D.expert_bias, E=wl.E, k=wl.k, stream=s)
+    plan = api.moe_plan(idx, E=wl.E, H=wl.H, I=wl.I, stream=s)
+    y = api.moe_experts(D.x, plan, w, D.W, E=wl.E, I=wl.I, combine=1, stream=s)
+    same([y, idx, w], want)
+
+
+def test_shared_expert(api, block):
+    wl, D = block
+    Ws = api.ExpertWeights(act=D.W.act, fmt=D.W.fmt, w1=D.W.w1[:1], w2=D.W.w2[:1])
+    want = api.moe_shared_expert(D.x, Ws, I=wl.I, combine=1)
+    s = torch.cuda.Stream()
+    n = api.moe_workspace_bytes(api.dims(wl.T, wl.H, 1, 1, wl.I), combine=1)
+    torch.cuda.synchronize()
+    freed_but_written_later(((wl.T, wl.H), torch.float32), ((n,), torch.uint8))
+    same([api.moe_shared_expert(D.x, Ws, I=wl.I, combine=1, stream=s)], [want])
