@@ -391,7 +391,10 @@ class DecodeLayer:
         n = moe_decode_workspace_bytes(d, Is)
         if n == 0:
             raise ValueError(f"sizes of the layer: {moe_last_error()}")
-        self.ws = torch.zeros(n, dtype=torch.uint8, device=dev)   # the first 256 bytes start at zero
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=dev)   # counts in the first 1 KB start at zero
+        with torch.cuda.device(dev):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()         # the first call may be on any stream
         self._layer = abi.moe_layer(_ptr(w_router), _ptr(expert_bias), W.c_struct(),
                                     Ws.c_struct() if Ws is not None else abi.moe_experts_w(), Is, eps, router_scale,
                                     out_scale, router_cfg(score, norm_topk))

@@ -90,3 +90,20 @@ def test_shared_expert(api, block):
     torch.cuda.synchronize()
     freed_but_written_later(((wl.T, wl.H), torch.float32), ((n,), torch.uint8))
     same([api.moe_shared_expert(D.x, Ws, I=wl.I, combine=1, stream=s)], [want])
+
+
+def test_layer_made_on_a_busy_stream_and_first_called_on_another(api, block):
+    """The workspace's counts are zero whichever stream calls first."""
+    wl, D = block
+    kw = dict(E=wl.E, k=wl.k, I=wl.I)
+    layer = api.DecodeLayer(D.W, D.w_router, D.expert_bias, **kw)
+    want, n = [t.clone() for t in layer(D.x)], layer.ws.numel()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(a):
+        torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")     # the block that the workspace will get
+        torch.cuda._sleep(CYCLES)
+        layer = api.DecodeLayer(D.W, D.w_router, D.expert_bias, **kw)
+        assert a.query()                                             # zeroed when the constructor returns
+    same(layer(D.x, stream=b), want)
+    assert api.moe_device_error() == 0
