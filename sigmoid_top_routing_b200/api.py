@@ -385,7 +385,8 @@ class DecodeLayer:
         if Ws is not None:
             _check_weights("Ws", Ws, 1, Is, self.H, dev)
         # the tensors themselves: W's and Ws' fields may be set to others later
-        self._keep = (dataclasses.replace(W), Ws and dataclasses.replace(Ws), w_router, expert_bias)
+        given = [w_router, expert_bias] + [getattr(w, f.name) for w in (W, Ws) if w for f in dataclasses.fields(w)]
+        self._tensors = [t for t in given if isinstance(t, torch.Tensor)]
         self.max_tokens = max_tokens
         d = abi.moe_dims(max_tokens, self.H, E, k, I)
         n = moe_decode_workspace_bytes(d, Is)
@@ -395,6 +396,7 @@ class DecodeLayer:
         with torch.cuda.device(dev):
             if not torch.cuda.is_current_stream_capturing():
                 torch.cuda.current_stream().synchronize()         # the first call may be on any stream
+        self._seen = {torch._C._cuda_getCurrentRawStream(dev.index)}   # streams that the allocator knows of
         self._layer = abi.moe_layer(_ptr(w_router), _ptr(expert_bias), W.c_struct(),
                                     Ws.c_struct() if Ws is not None else abi.moe_experts_w(), Is, eps, router_scale,
                                     out_scale, router_cfg(score, norm_topk))
@@ -445,9 +447,15 @@ class DecodeLayer:
         return y, topk_idx, topk_w
 
     def _go(self, plan, x, logits, residual, topk_idx, topk_w, y, stream):
+        raw = _stream_on(stream, self.device.index)
+        if raw not in self._seen:                                 # a dropped layer's memory waits for this stream
+            s = torch.cuda.ExternalStream(raw, device=self.device)
+            for t in (self.ws, *self._tensors):
+                t.record_stream(s)
+            self._seen.add(raw)
         return self._run(plan, x.data_ptr(), None if logits is None else logits.data_ptr(),
                          None if residual is None else residual.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(),
-                         y.data_ptr(), self.ws.data_ptr(), self.ws.numel(), _stream_on(stream, self.device.index))
+                         y.data_ptr(), self.ws.data_ptr(), self.ws.numel(), raw)
 
 
 def moe_profile_hook(ev_begin, ev_end, stage: int) -> None:

@@ -107,3 +107,20 @@ def test_layer_made_on_a_busy_stream_and_first_called_on_another(api, block):
         assert a.query()                                             # zeroed when the constructor returns
     same(layer(D.x, stream=b), want)
     assert api.moe_device_error() == 0
+
+
+def test_workspace_outlives_its_layer_on_another_stream(api, block):
+    """The layer is dropped while a call of it waits on a side stream; its workspace is not handed out."""
+    wl, D = block
+    kw = dict(E=wl.E, k=wl.k, I=wl.I)
+    layer = api.DecodeLayer(D.W, D.w_router, D.expert_bias, **kw)
+    want = [t.clone() for t in layer(D.x)]
+    n, at, s = layer.ws.numel(), layer.ws.data_ptr(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(CYCLES)
+    got = layer(D.x, stream=s)
+    del layer
+    blocks = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert at not in [t.data_ptr() for t in blocks]
+    same(got, want)
