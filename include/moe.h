@@ -318,8 +318,9 @@ MOE_API moe_status moe_shared_expert_ex(const void* x, const moe_experts_w* Ws, 
  * call and the library's from then on (it holds counts that carry over from call
  * to call).  It may serve any layer whose sizes need no more of it.  Calls that share it
  * must run on one device and not overlap on the GPU.  The launch is cooperative
- * (one CTA per SM, all resident); waits between CTAs are bounded and report
- * device error 2 (zero-fill the workspace again after it). */
+ * (one CTA per SM, all resident); its waits are bounded: where one runs out the
+ * call records device error 2 and ends without writing y, topk_idx and topk_w are
+ * undefined, and the workspace serves the next call as it is. */
 #define MOE_DECODE_MAX_T 16
 typedef struct {
     const float* w_router;
@@ -345,6 +346,12 @@ MOE_API moe_status moe_decode_prepare(const moe_layer* L, const moe_dims* d, moe
 MOE_API moe_status moe_decode_run(const moe_decode_plan* plan, const void* x, const float* logits,
                                   const void* residual, int32_t* topk_idx, float* topk_w, void* y, void* ws,
                                   size_t ws_bytes, moe_stream_t stream);
+/* moe_decode_run with the failure that its bounded waits are for, made without a
+ * fault (as moe_wait_bound_check): the grid barriers wait for one arrival more than
+ * comes and give up after `polls` polls, 1 to 2^20 (MOE_ERR_SHAPE). */
+MOE_API moe_status moe_decode_expiry_check(const moe_decode_plan* plan, const void* x, const float* logits,
+                                           const void* residual, int32_t* topk_idx, float* topk_w, void* y,
+                                           void* ws, size_t ws_bytes, uint32_t polls, moe_stream_t stream);
 MOE_API size_t moe_decode_workspace_bytes(const moe_dims* d, int32_t Is);
 /* Shared memory of moe_decode's CTAs for these sizes and a device whose CTAs may
  * have smem_bytes of it (for inspection and tests: no device is needed).  Offsets
@@ -495,8 +502,8 @@ MOE_API moe_status moe_wait_bound_check(uint32_t polls, moe_stream_t stream);
 
 /* Synchronises `stream`, then reads and clears the device error word of the
  * current device.  *code = 0 when no kernel reported an error.  Codes:
- * 1 expert id out of range in moe_plan; 2 a bounded pipeline wait expired in
- * a grouped GEMM kernel.  Returns MOE_ERR_DEVICE when *code != 0. */
+ * 1 expert id out of range in moe_plan; 2 a bounded wait expired in a grouped
+ * GEMM kernel, moe_decode or moe_linear.  Returns MOE_ERR_DEVICE when *code != 0. */
 MOE_API moe_status moe_device_error(int32_t* code, moe_stream_t stream);
 
 /* Message for the calling thread's last non-OK status ("" if none). */

@@ -120,6 +120,8 @@ PROTOTYPES = {
     "moe_decode_prepare": (c_int32, [POINTER(moe_layer), POINTER(moe_dims), POINTER(moe_decode_plan)]),
     "moe_decode_run": (c_int32, [POINTER(moe_decode_plan), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                  c_void_p, c_size_t, c_void_p]),
+    "moe_decode_expiry_check": (c_int32, [POINTER(moe_decode_plan), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                          c_void_p, c_void_p, c_size_t, ctypes.c_uint32, c_void_p]),
     "moe_decode": (c_int32, [POINTER(moe_layer), POINTER(moe_dims), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                              c_void_p, c_void_p, c_size_t, c_void_p]),
     "moe_forward_host": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, POINTER(moe_dims), c_float,

@@ -123,7 +123,8 @@ struct DecodeArgs {
     Divisor by_ysplit, by_yworkers;
     float2* ypart;                              // (ysplit, T, H): sums of the routed and the shared experts
     int* ydone;                                 // per block: CTAs that wrote theirs; zero between calls
-    uint32_t wait_limit;
+    uint32_t wait_limit;                        // polls of a ring wait
+    uint32_t grid_limit, missing;               // polls of a grid barrier; arrivals it waits for in vain (0 but in the expiry check)
     int* err;
 };
 
@@ -660,7 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         bool dead = false;
         // Grid barrier: arrivals only ever add up, gridDim.x per barrier, so what
         // is there when a CTA looks, rounded down to a multiple of that, is where
-        // the count stood before its next own arrival.
+        // the count stood before its next own arrival.  A CTA whose wait runs out goes
+        // on to the end and arrives at every barrier: the counts are whole after it.
         unsigned long long seen = 0, target = 0;
         if (tid == 0) asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(seen) : "l"(a.sync) : "memory");
         // thread 0: the release covers what it and, through the CTA's barrier just
@@ -671,10 +673,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         };
         auto grid_wait = [&]() {                // thread 0
             bool ok = false;
-            for (uint32_t i = 0; i < a.wait_limit && !ok; ++i) {
+            for (uint32_t i = 0; i < a.grid_limit && !ok; ++i) {
                 unsigned long long v;
                 asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(a.sync) : "memory");
-                ok = v >= target;
+                ok = v >= target + a.missing;
             }
             if (!ok) {
                 report_error(a.err, kErrWaitExpired);
@@ -952,7 +954,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&empty[s]);
+                    // (after a wait that ran out the slot's copies may still be under way: it
+                    // is not released, and the producer, which then stops, fills it no more)
+                    if (lane == 0 && !dead) mbar_arrive(&empty[s]);
                     if (++slot == Sg) {
                         slot = 0;
                         ph ^= 1;
@@ -1280,6 +1284,44 @@ moe_status check_call(const void* x, const float* logits, const float* w_router,
     return MOE_OK;
 }
 
+// A prepared call; polls > 0: with grid barriers that run out after that many.
+moe_status run(const moe_decode_plan* plan, const void* x, const float* logits, const void* residual, int32_t* topk_idx,
+               float* topk_w, void* y, void* ws, size_t ws_bytes, uint32_t polls, moe_stream_t stream) {
+    if (!plan) return refuse(MOE_ERR_NULL, "plan is NULL");
+    Plan p;
+    memcpy(&p, plan, sizeof p);
+    if (p.magic != kPlanMagic) return refuse(MOE_ERR_UNSUPPORTED, "not a plan of moe_decode_prepare");
+    if (p.a.T == 0) return set_last_launch_count(0), MOE_OK;   // empty batch: nothing to do
+    const moe_status st = check_call(x, logits, p.a.w_router, residual, topk_idx, topk_w, y, ws, ws_bytes, p.ws_bytes,
+                                     (size_t)p.a.T * p.a.H * 2);
+    if (st != MOE_OK) return st;
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev != p.device)
+        return refuse(MOE_ERR_UNSUPPORTED, "the plan was prepared for another device");
+    if (polls) {
+        p.a.grid_limit = polls;
+        p.a.missing = 1;
+    }
+    char* b = static_cast<char*>(ws);
+    p.a.x = static_cast<const uint16_t*>(x);
+    p.a.logits = logits;
+    p.a.residual = static_cast<const uint16_t*>(residual);
+    p.a.idx = topk_idx;
+    p.a.w = topk_w;
+    p.a.y = static_cast<uint16_t*>(y);
+    p.a.sync = reinterpret_cast<unsigned long long*>(b);
+    p.a.lg = reinterpret_cast<float2*>(b + p.ws_lg);
+    p.a.h = reinterpret_cast<uint16_t*>(b + p.ws_h);
+    p.a.hs = reinterpret_cast<uint16_t*>(b + p.ws_hs);
+    p.a.ypart = reinterpret_cast<float2*>(b + p.ws_yp);
+    p.a.ydone = reinterpret_cast<int*>(b + 256);
+    if (e == cudaSuccess) e = p.launch(p, p.a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return refuse(MOE_ERR_CUDA, cudaGetErrorString(e));
+    set_last_launch_count(1);
+    return MOE_OK;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -1352,7 +1394,7 @@ moe_status moe_decode_prepare(const moe_layer* L, const moe_dims* d, moe_decode_
     a.limit = L->W.swiglu_limit;
     a.softmax = L->router.score == MOE_SCORE_SOFTMAX;
     a.no_norm = L->router.norm_topk == 0;
-    a.wait_limit = sm100::kWaitLimit;
+    a.wait_limit = a.grid_limit = sm100::kWaitLimit;
     a.err = device_info().err_word;
     p.ws_bytes = wl.total;
     p.ws_lg = wl.lg;
@@ -1374,35 +1416,15 @@ moe_status moe_decode_prepare(const moe_layer* L, const moe_dims* d, moe_decode_
 
 moe_status moe_decode_run(const moe_decode_plan* plan, const void* x, const float* logits, const void* residual,
                           int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes, moe_stream_t stream) {
-    if (!plan) return refuse(MOE_ERR_NULL, "plan is NULL");
-    Plan p;
-    memcpy(&p, plan, sizeof p);
-    if (p.magic != kPlanMagic) return refuse(MOE_ERR_UNSUPPORTED, "not a plan of moe_decode_prepare");
-    if (p.a.T == 0) return set_last_launch_count(0), MOE_OK;   // empty batch: nothing to do
-    const moe_status st = check_call(x, logits, p.a.w_router, residual, topk_idx, topk_w, y, ws, ws_bytes, p.ws_bytes,
-                                     (size_t)p.a.T * p.a.H * 2);
-    if (st != MOE_OK) return st;
-    int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && dev != p.device)
-        return refuse(MOE_ERR_UNSUPPORTED, "the plan was prepared for another device");
-    char* b = static_cast<char*>(ws);
-    p.a.x = static_cast<const uint16_t*>(x);
-    p.a.logits = logits;
-    p.a.residual = static_cast<const uint16_t*>(residual);
-    p.a.idx = topk_idx;
-    p.a.w = topk_w;
-    p.a.y = static_cast<uint16_t*>(y);
-    p.a.sync = reinterpret_cast<unsigned long long*>(b);
-    p.a.lg = reinterpret_cast<float2*>(b + p.ws_lg);
-    p.a.h = reinterpret_cast<uint16_t*>(b + p.ws_h);
-    p.a.hs = reinterpret_cast<uint16_t*>(b + p.ws_hs);
-    p.a.ypart = reinterpret_cast<float2*>(b + p.ws_yp);
-    p.a.ydone = reinterpret_cast<int*>(b + 256);
-    if (e == cudaSuccess) e = p.launch(p, p.a, reinterpret_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return refuse(MOE_ERR_CUDA, cudaGetErrorString(e));
-    set_last_launch_count(1);
-    return MOE_OK;
+    return run(plan, x, logits, residual, topk_idx, topk_w, y, ws, ws_bytes, 0, stream);
+}
+
+moe_status moe_decode_expiry_check(const moe_decode_plan* plan, const void* x, const float* logits,
+                                   const void* residual, int32_t* topk_idx, float* topk_w, void* y, void* ws,
+                                   size_t ws_bytes, uint32_t polls, moe_stream_t stream) {
+    if (polls < 1 || polls > (1u << 20))
+        return refuse(MOE_ERR_SHAPE, "moe_decode_expiry_check: polls must be in [1, 2^20]");
+    return run(plan, x, logits, residual, topk_idx, topk_w, y, ws, ws_bytes, polls, stream);
 }
 
 moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void* x, const float* logits,

@@ -197,3 +197,12 @@ def test_boxed_scales_start_on_their_swizzle_period(lib, fmt, period):
                 assert all(s % period == 0 for s in starts), (T, H, I, Is, st.scales, st.area)
                 boxes += 1
     assert boxes > 50000
+
+
+@pytest.mark.parametrize("polls", [0, (1 << 20) + 1])
+def test_expiry_check_refuses_its_polls(lib, polls):
+    plan = abi.moe_decode_plan()
+    args = (0x10000, None, None, 0x20000, 0x30000, 0x40000, 0x1000000, 1 << 24)
+    assert lib.moe_decode_expiry_check(ctypes.byref(plan), *args, polls, None) == abi.MOE_ERR_SHAPE
+    assert lib.moe_decode_expiry_check(ctypes.byref(plan), *args, 1, None) == abi.MOE_ERR_UNSUPPORTED   # no plan
+    assert lib.moe_decode_expiry_check(None, *args, 1, None) == abi.MOE_ERR_NULL

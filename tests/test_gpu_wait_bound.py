@@ -44,3 +44,37 @@ def test_expired_wait_reports_code_2_and_context_survives(api):
     assert np.array_equal(idx.cpu().numpy(), ref["idx"])
     yg = y.float().cpu().numpy().astype(np.float64)
     assert np.linalg.norm(yg - ref["y"]) / np.linalg.norm(ref["y"]) < 1e-2
+
+
+@pytest.mark.parametrize("polls", [1, 4096])
+@pytest.mark.parametrize("fmt,T,shared_I,given", [("bf16", 8, 0, False), ("bf16", 2, 128, True), ("affine4", 9, 320, False),
+                                                  ("nvfp4", 16, 64, False), ("nvfp4", 1, 0, True)])
+def test_decode_layer_whose_grid_barriers_run_out(api, fmt, T, shared_I, given, polls):
+    """The call records error 2 and ends, y keeps its bytes, and the next call with the
+    same workspace has the same bits as before."""
+    import ctypes
+
+    from sigmoid_top_routing_b200 import abi, inputs
+    from sigmoid_top_routing_b200.device_inputs import shared_to_device, to_device
+    wl = inputs.Workload("expiry", T=T, H=320, E=24, k=5, I=704, fmt=fmt, shared_I=shared_I)
+    inp = inputs.make_inputs(wl)
+    D, Ws = to_device(inp), shared_to_device(inp)
+    layer = api.DecodeLayer(D.W, D.w_router, D.expert_bias, E=wl.E, k=wl.k, I=wl.I, Ws=Ws, Is=shared_I)
+    logits = torch.randn(T, wl.E, device="cuda") if given else None
+    want = [t.clone() for t in layer(D.x, logits=logits)]
+    G = torch.cuda.get_device_properties(0).multi_processor_count
+    y = torch.full_like(want[0], 7.0)
+    idx, w = torch.empty_like(want[1]), torch.empty_like(want[2])
+    for _ in range(2):
+        st = api.load().moe_decode_expiry_check(
+            layer._plans[T][1], D.x.data_ptr(), None if logits is None else logits.data_ptr(), None, idx.data_ptr(),
+            w.data_ptr(), y.data_ptr(), layer.ws.data_ptr(), layer.ws.numel(), polls,
+            torch.cuda.current_stream().cuda_stream)
+        assert st == abi.MOE_OK
+        torch.cuda.synchronize()
+        assert api.moe_device_error() == 2
+        assert (y == 7.0).all()
+        assert int(layer.ws[:8].view(torch.int64)) % G == 0 and (layer.ws[8:1024] == 0).all()
+        for a, b in zip(layer(D.x, logits=logits), want):
+            assert torch.equal(a, b)
+        assert api.moe_device_error() == 0
