@@ -307,7 +307,9 @@ MOE_API moe_status moe_shared_expert_ex(const void* x, const moe_experts_w* Ws, 
  *   x           bf16 (T, H).  Routing reads x, or logits (fp32 (T, E)) when given.
  *   residual    bf16 (T, H) or NULL, added to the finished sum in fp32.
  *   topk_idx, topk_w, y   outputs as of moe_forward_ex.  y may be residual or x
- *               (a residual that y overlaps in part is MOE_ERR_UNSUPPORTED).
+ *               (a residual that y overlaps in part is MOE_ERR_UNSUPPORTED, and so is
+ *               any other overlap of an output with the other outputs or the workspace,
+ *               and of topk_idx or topk_w with x, logits or residual).
  * Sizes: moe_dims' limits, T <= MOE_DECODE_MAX_T and T * H <= 65536
  * (MOE_ERR_SHAPE otherwise: moe_forward takes those).
  * Arithmetic: logits, scores and weights in 64-bit (topk_w rounded once to fp32),

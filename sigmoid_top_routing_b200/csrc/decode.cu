@@ -1263,10 +1263,16 @@ moe_status check_layer(const moe_layer* L, const moe_dims* d) {
     return MOE_OK;
 }
 
-// What a call brings.
+// Whether n bytes at p and m at q share one.
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + m && b < a + n;
+}
+
+// What a call of T tokens brings.
 moe_status check_call(const void* x, const float* logits, const float* w_router, const void* residual,
                       const int32_t* topk_idx, const float* topk_w, const void* y, const void* ws, size_t ws_bytes,
-                      size_t need, size_t row_bytes) {
+                      size_t need, int T, int H, int E, int k) {
     if (!x || !y) return refuse(MOE_ERR_NULL, "x or y is NULL");
     if (!topk_idx || !topk_w) return refuse(MOE_ERR_NULL, "topk_idx or topk_w is NULL");
     if (!logits && !w_router) return refuse(MOE_ERR_NULL, "w_router is NULL (routing from x)");
@@ -1274,13 +1280,22 @@ moe_status check_call(const void* x, const float* logits, const float* w_router,
     if (misaligned(residual, 16)) return refuse(MOE_ERR_ALIGN, "residual not 16-byte aligned");
     if (misaligned(logits, 4) || misaligned(topk_idx, 4) || misaligned(topk_w, 4))
         return refuse(MOE_ERR_ALIGN, "logits, topk_idx or topk_w not 4-byte aligned");
-    // (x may lie anywhere in y: every CTA has its copy before the first store to y)
-    const uintptr_t py = reinterpret_cast<uintptr_t>(y), pr = reinterpret_cast<uintptr_t>(residual);
-    if (residual && pr != py && pr < py + row_bytes && py < pr + row_bytes)
+    // (x and logits may lie anywhere in y: they are read before the second grid barrier, y is written behind it)
+    const size_t rows = (size_t)T * H * 2, picks = (size_t)T * k * 4;
+    if (residual != y && overlap(residual, rows, y, rows))
         return refuse(MOE_ERR_UNSUPPORTED, "moe_decode: y overlaps a part of residual (it may be residual itself)");
     if (!ws) return refuse(MOE_ERR_WORKSPACE, "workspace is NULL");
     if (misaligned(ws, 256)) return refuse(MOE_ERR_ALIGN, "workspace not 256-byte aligned");
     if (ws_bytes < need) return refuse(MOE_ERR_WORKSPACE, "workspace smaller than moe_decode_workspace_bytes()");
+    // the picks are written while other CTAs still read x and logits, topk_w is read back
+    const void* outs[3] = {topk_idx, topk_w, y};
+    for (int i = 0; i < 3; ++i) {
+        const size_t n = i < 2 ? picks : rows;
+        const bool in = i < 2 && (overlap(outs[i], n, x, rows) || overlap(outs[i], n, residual, rows) ||
+                                  overlap(outs[i], n, logits, (size_t)T * E * 4));
+        if (in || overlap(outs[i], n, outs[(i + 1) % 3], i == 1 ? rows : picks) || overlap(outs[i], n, ws, need))
+            return refuse(MOE_ERR_UNSUPPORTED, "moe_decode: topk_idx, topk_w or y overlaps another argument");
+    }
     return MOE_OK;
 }
 
@@ -1293,7 +1308,7 @@ moe_status run(const moe_decode_plan* plan, const void* x, const float* logits, 
     if (p.magic != kPlanMagic) return refuse(MOE_ERR_UNSUPPORTED, "not a plan of moe_decode_prepare");
     if (p.a.T == 0) return set_last_launch_count(0), MOE_OK;   // empty batch: nothing to do
     const moe_status st = check_call(x, logits, p.a.w_router, residual, topk_idx, topk_w, y, ws, ws_bytes, p.ws_bytes,
-                                     (size_t)p.a.T * p.a.H * 2);
+                                     p.a.T, p.a.H, p.a.E, p.a.k);
     if (st != MOE_OK) return st;
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1434,7 +1449,7 @@ moe_status moe_decode(const moe_layer* L, const moe_dims* d, const void* x, cons
     if (st != MOE_OK) return st;
     if (d->T == 0) return set_last_launch_count(0), MOE_OK;   // empty batch: nothing to do
     st = check_call(x, logits, L->w_router, residual, topk_idx, topk_w, y, ws, ws_bytes, ws_layout(d, L->Is).total,
-                    (size_t)d->T * d->H * 2);
+                    d->T, d->H, d->E, d->k);
     if (st != MOE_OK) return st;
     moe_decode_plan plan;
     st = moe_decode_prepare(L, d, &plan);

@@ -206,3 +206,14 @@ def test_expiry_check_refuses_its_polls(lib, polls):
     assert lib.moe_decode_expiry_check(ctypes.byref(plan), *args, polls, None) == abi.MOE_ERR_SHAPE
     assert lib.moe_decode_expiry_check(ctypes.byref(plan), *args, 1, None) == abi.MOE_ERR_UNSUPPORTED   # no plan
     assert lib.moe_decode_expiry_check(None, *args, 1, None) == abi.MOE_ERR_NULL
+
+
+# T = 4, H = 256, E = 8, k = 2: x, residual and y are 2048 bytes, logits 128, picks 32
+@pytest.mark.parametrize("over", [
+    dict(idx=0x10000), dict(idx=0x10000 + 2044), dict(w=0x10000 - 28), dict(residual=0x60000, w=0x60400),
+    dict(logits=0x60000, idx=0x60000), dict(logits=0x60000, w=0x60000 + 124), dict(idx=0x30000), dict(w=0x20000 + 28),
+    dict(w=0x40000), dict(idx=0x40000 + 2044), dict(idx=0x40000 - 28), dict(y=0x1000000), dict(w=0x1000100),
+])
+def test_picks_over_other_arguments(lib, over):
+    assert _call(lib, **over) == abi.MOE_ERR_UNSUPPORTED
+    assert b"overlaps" in lib.moe_last_error()
