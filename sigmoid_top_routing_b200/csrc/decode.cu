@@ -165,13 +165,15 @@ MOE_DEV float unkey32(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7ff
 MOE_DEV double sigmoid64(double L) { return 1.0 / (1.0 + exp(-L)); }
 
 // Unevaluated fp32 sums hi + lo (about 46 bits), for the router's dot products:
-// double-precision arithmetic runs at a small fraction of the fp32 rate.
+// double-precision arithmetic runs at a small fraction of the fp32 rate.  (The _rn
+// functions are never contracted: a product fused into the next sum would no longer be
+// the one whose error is kept.)
 struct F2 {
     float hi, lo;
 };
 MOE_DEV void add_to(F2& a, float v) {           // a += v, error-free in hi
-    const float s = a.hi + v, t = s - a.hi;
-    a.lo += (a.hi - (s - t)) + (v - t);
+    const float s = __fadd_rn(a.hi, v), t = __fsub_rn(s, a.hi);
+    a.lo += __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(v, t));
     a.hi = s;
 }
 MOE_DEV void add_to(F2& a, F2 b) {
@@ -179,7 +181,7 @@ MOE_DEV void add_to(F2& a, F2 b) {
     a.lo += b.lo;
 }
 MOE_DEV void fma_to(F2& a, float x, float y) {  // a += x y, the product's rounding error kept
-    const float p = x * y;
+    const float p = __fmul_rn(x, y);
     const float e = fmaf(x, y, -p);
     add_to(a, p);
     a.lo += e;
