@@ -461,3 +461,48 @@ def test_layer_keeps_the_tensors_it_was_given(api, fmt):
         for a, b in zip(layer(x[:T]), want):
             assert torch.equal(a, b[:T])
     del junk
+
+
+def comparable_residual(wl, ref_y):
+    """bf16 residual of about the experts' own size (a power of two times N(0, 1)): an
+    error of their sum is not drowned by the residual's own rounding."""
+    rms = np.sqrt(np.mean(ref_y ** 2))
+    r = np.random.default_rng(9).standard_normal((wl.T, wl.H)) * 2.0 ** np.round(np.log2(rms))
+    return G.f32_to_bf16_bits(r.astype(np.float32))
+
+
+def strict_gate(got, ref_y, residual=None):
+    """Norm of the error against the roundings': y's, at most U of what is stored, and the
+    activations', whose independent relative errors of at most U each reach at most U of
+    the experts' sum when it does not cancel systematically."""
+    want = ref_y + (O.bf16_to_f64(residual) if residual is not None else 0.0)
+    err, gate = np.linalg.norm(got - want), U * (np.linalg.norm(want) + np.linalg.norm(ref_y))
+    assert err <= gate, err / gate
+
+
+def test_the_gate_sees_a_missing_or_scaled_part():
+    """The gate on the oracle's own values: a twentieth too little, or no residual, fails it."""
+    ref = np.random.default_rng(1).standard_normal((8, 256)) * 1e-3
+    wl = W("gate", T=8, H=256, E=1, k=1, I=64)
+    r = comparable_residual(wl, ref)
+    full = ref + O.bf16_to_f64(r)
+    strict_gate(full, ref, r)
+    for bad in (ref, O.bf16_to_f64(r), full - 0.05 * ref):
+        with pytest.raises(AssertionError):
+            strict_gate(bad, ref, r)
+    with pytest.raises(AssertionError):
+        strict_gate(0.97 * ref, ref)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "affine4", "nvfp4"])
+@pytest.mark.parametrize("wl", next(m.args[1] for m in test_parity.pytestmark if m.args[0] == "wl"), ids=lambda w: w.name)
+def test_experts_alone_and_beside_a_residual_of_their_size(api, wl, fmt):
+    inp = inputs_of(dataclasses.replace(wl, fmt=fmt, name=f"{wl.name}_{fmt}"))
+    D, layer = make_layer(api, inp)
+    from sigmoid_top_routing_b200.device_inputs import bf16_tensor
+    ref = O.moe_block(inp)
+    res = comparable_residual(wl, ref["y"])
+    for r in (None, res):
+        y, idx, w = layer(D.x, residual=None if r is None else bf16_tensor(r, "cuda"))
+        compare(inp, bits(y), idx.cpu().numpy(), w.cpu().numpy(), r)
+        strict_gate(O.bf16_to_f64(bits(y)), ref["y"], r)

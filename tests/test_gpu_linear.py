@@ -267,3 +267,17 @@ def test_layers_of_a_hybrid_stack(api):
     assert torch.equal(idx, idx2)
     moe = torch.from_numpy(ref["y"]).cuda()
     assert (y2.double() - moe).norm() <= 3 * 2.0 ** -8 * moe.norm()   # h and hs rounded, then y
+
+
+@pytest.mark.parametrize("M,act", [(4, "relu2"), (512, "relu2"), (512, "swiglu"), (512, "none"), (2000, "relu2")])
+def test_rows_beside_nan_and_infinite_rows(api, M, act):
+    """Tokens whose tile also holds a NaN and an infinite token keep to the formula's bound."""
+    x, w, b, r = make(M, 600, 128, act, bias=True, residual=torch.bfloat16, seed=6)
+    x = x.clone()
+    x[1] = float("nan")
+    x[2, 3] = float("inf")
+    y = api.moe_linear(x, w, b, r, act=act)
+    rows = [i for i in range(M) if i not in (1, 2)]
+    want, tol = formula(x[rows], w, b, r[rows], act, 0.0, torch.bfloat16)
+    assert torch.isnan(y[1]).all()
+    assert ((y[rows].double() - want).abs() <= tol).all()
