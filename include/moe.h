@@ -413,6 +413,13 @@ typedef struct {
 } moe_linear_cfg;
 MOE_API moe_status moe_linear(const void* x, const void* w, const float* bias, const void* residual,
                               const moe_linear_dims* d, const moe_linear_cfg* cfg, void* y, moe_stream_t stream);
+/* moe_linear with the failure that its bounded waits are for, made without a fault (as
+ * moe_wait_bound_check): the tensor-core warp first waits for something that never
+ * comes and gives up after `polls` polls, 1 to 2^20 (MOE_ERR_SHAPE).  The call records
+ * device error 2 and ends; y is not written. */
+MOE_API moe_status moe_linear_expiry_check(const void* x, const void* w, const float* bias, const void* residual,
+                                           const moe_linear_dims* d, const moe_linear_cfg* cfg, void* y,
+                                           uint32_t polls, moe_stream_t stream);
 
 /* moe_forward with HOST buffers for the token rows: x_host (T, H) bf16 is
  * copied to x_dev, the block runs, and y_dev is copied back to y_host (T, H)

@@ -115,6 +115,8 @@ PROTOTYPES = {
                                        POINTER(moe_exec_cfg), c_void_p, c_void_p, c_size_t, c_void_p]),
     "moe_linear": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, POINTER(moe_linear_dims), POINTER(moe_linear_cfg),
                              c_void_p, c_void_p]),
+    "moe_linear_expiry_check": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, POINTER(moe_linear_dims),
+                                          POINTER(moe_linear_cfg), c_void_p, ctypes.c_uint32, c_void_p]),
     "moe_decode_workspace_bytes": (c_size_t, [POINTER(moe_dims), c_int32]),
     "moe_decode_smem_layout": (c_int32, [POINTER(moe_dims), c_int32, c_int32, c_int32, POINTER(moe_decode_smem)]),
     "moe_decode_prepare": (c_int32, [POINTER(moe_layer), POINTER(moe_dims), POINTER(moe_decode_plan)]),

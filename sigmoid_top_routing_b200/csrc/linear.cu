@@ -65,7 +65,7 @@ struct LinParams {
     int stages, ks;
     int res_f32, y_f32;
     float limit;
-    uint32_t wait_limit;
+    uint32_t hold;                               // > 0 (the expiry check): the MMA warp first waits this long for nothing
     int* err;
 };
 
@@ -193,6 +193,10 @@ MOE_DEV void tma_load_3d_pair(void* dst, const CUtensorMap* m, int x, int y, int
         : "memory");
 }
 
+MOE_DEV void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // Tile t of the persistent order: weight tiles in groups of 8, token tiles
 // within a group, so the tiles running at one time share operands in L2.
 MOE_DEV void tile_of(const LinParams& p, int t, int& wt, int& tt) {
@@ -255,6 +259,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     pdl_wait();
     pdl_trigger();
     const int total = p.n_wt * p.n_tt, tbeg = blockIdx.x >> 1, tstep = gridDim.x >> 1;
+    // A wait ran out: neither CTA of the pair can go on without the other.
+    auto give_up = [&]() {
+        if (lane == 0) report_error(p.err, kErrWaitExpired);
+        *s_abort = 1;
+        st_cluster_u32(mapa_shared(smem_u32(const_cast<const int*>(s_abort)), rank ^ 1u), 1u);
+    };
     if (warp == 0) {
         int s = 0;
         uint32_t ph = 0, issued = 0, par = 0;
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             tile_of(p, t, wt, tt);
             const int f0 = (wt * 2 + (int)rank) * kF, row = tt * p.BN + (int)rank * (p.BN / 2);
             for (int kb = 0; kb < p.nkb; kb += 2) {      // k past the end is zero-filled
-                if (!warp_wait(&empty[s], ph ^ 1, s_abort, p.wait_limit)) { ok = false; break; }
+                if (!warp_wait(&empty[s], ph ^ 1, s_abort, kWaitLimit)) { ok = false; break; }
                 if (elect_one()) {
                     // both CTAs' loads complete on the even CTA's barrier, which arrives once
                     const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
@@ -289,26 +299,23 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 if (++s == S) { s = 0; ph ^= 1; }
             }
         }
-        if (!ok) {
-            if (lane == 0) report_error(p.err, kErrWaitExpired);
-            *s_abort = 1;
-        }
+        if (!ok) give_up();
         if (rank == 0)                           // counts the odd CTA's bytes too
             for (int q = 0; q < S; ++q)
-                if (issued >> q & 1u) mbar_wait(&full[q], par >> q & 1u, nullptr, p.wait_limit);
+                if (issued >> q & 1u) mbar_wait(&full[q], par >> q & 1u, nullptr, kWaitLimit);
     } else if (warp == 1) {
         if (rank == 0) {
             int s = 0, it = 0;
             uint32_t ph = 0;
-            bool ok = true;
+            bool ok = !p.hold || warp_wait(drain, 0, nullptr, p.hold);   // (nothing is committed to it yet)
             const uint32_t idesc = idesc_bf16(256, p.BN);
             for (int t = tbeg; t < total && ok; t += tstep, ++it) {
                 const int buf = it & 1;
-                if (!warp_wait(&tempty[buf], ((it >> 1) & 1) ^ 1, s_abort, p.wait_limit)) { ok = false; break; }
+                if (!warp_wait(&tempty[buf], ((it >> 1) & 1) ^ 1, s_abort, kWaitLimit)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem + buf * 256;
                 for (int kb = 0; kb < p.nkb; kb += 2) {
-                    if (!warp_wait(&full[s], ph, s_abort, p.wait_limit)) { ok = false; break; }
+                    if (!warp_wait(&full[s], ph, s_abort, kWaitLimit)) { ok = false; break; }
                     tc_fence_after();
                     const uint64_t ad = sdesc_sw128(smem_u32(sA + s * kPairA));
                     const uint64_t bd = sdesc_sw128(smem_u32(sB + s * bstage));
@@ -329,13 +336,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     if (++s == S) { s = 0; ph ^= 1; }
                 }
             }
-            if (!ok) {
-                if (lane == 0) report_error(p.err, kErrWaitExpired);
-                *s_abort = 1;
-            }
+            if (!ok) give_up();
             if (elect_one()) umma_commit_pair_local(drain);
             __syncwarp();
-            mbar_wait(drain, 0, nullptr, p.wait_limit);
+            mbar_wait(drain, 0, nullptr, kWaitLimit);
         }
         __syncwarp();
     } else {
@@ -349,10 +353,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             float b0, b1;
             bias_of<ACT>(p, f, b0, b1);
             if (!dead) {
-                const bool ok = mbar_wait(&tfull[buf], (it >> 1) & 1, s_abort, p.wait_limit);
+                const bool ok = mbar_wait(&tfull[buf], (it >> 1) & 1, s_abort, kWaitLimit);
                 if (__any_sync(0xffffffffu, !ok)) {
-                    if (lane == 0) report_error(p.err, kErrWaitExpired);
-                    *s_abort = 1;
+                    give_up();
                     dead = true;
                 }
             }
@@ -435,7 +438,7 @@ __global__ void __launch_bounds__(kLinThreads)
         bool ok = true;
         const uint64_t pol = policy_evict_first();               // weights of a single token tile are read once
         for (int kb = kb0; kb < kb1; ++kb) {
-            if (!warp_wait(&empty[s], ph ^ 1, &s_abort, p.wait_limit)) { ok = false; break; }
+            if (!warp_wait(&empty[s], ph ^ 1, &s_abort, kWaitLimit)) { ok = false; break; }
             if (elect_one()) {
                 mbar_arrive_expect_tx(&full[s], kAStage + bstage);
                 unsigned char* a = sA + s * kAStage;
@@ -459,14 +462,14 @@ __global__ void __launch_bounds__(kLinThreads)
             s_abort = 1;
         }
         for (int q = 0; q < S; ++q)
-            if (issued >> q & 1u) mbar_wait(&full[q], par >> q & 1u, nullptr, p.wait_limit);
+            if (issued >> q & 1u) mbar_wait(&full[q], par >> q & 1u, nullptr, kWaitLimit);
     } else if (warp == 1) {
         int s = 0;
         uint32_t ph = 0;
-        bool ok = true;
+        bool ok = !p.hold || warp_wait(&done, 0, nullptr, p.hold);   // (nothing is committed to it yet)
         const uint32_t idesc = idesc_bf16(128, p.BN);
-        for (int kb = kb0; kb < kb1; ++kb) {
-            if (!warp_wait(&full[s], ph, &s_abort, p.wait_limit)) { ok = false; break; }
+        for (int kb = kb0; kb < kb1 && ok; ++kb) {
+            if (!warp_wait(&full[s], ph, &s_abort, kWaitLimit)) { ok = false; break; }
             tc_fence_after();
             const uint64_t ad = sdesc_sw128(smem_u32(sA + s * kAStage));
             const uint64_t bd = sdesc_sw128(smem_u32(sB + s * bstage));
@@ -489,7 +492,7 @@ __global__ void __launch_bounds__(kLinThreads)
     }
     __syncwarp();
     // The accumulator is complete, and with it every load has been consumed.
-    const bool ok = mbar_wait(&done, 0, nullptr, p.wait_limit);
+    const bool ok = mbar_wait(&done, 0, nullptr, kWaitLimit);
     if (!ok) s_abort = 1;
     __syncthreads();
     tc_fence_after();
@@ -694,13 +697,9 @@ bool overlap(const Span& a, const Span& b) {
     return off < lo.row || off + hi.row > pitch;
 }
 
-}  // namespace
-}  // namespace moe
-
-using namespace moe;
-
-extern "C" moe_status moe_linear(const void* x, const void* w, const float* bias, const void* residual,
-                                 const moe_linear_dims* d, const moe_linear_cfg* cfg, void* y, moe_stream_t stream) {
+// A call; hold > 0: whose first wait runs out after that many polls.
+moe_status linear(const void* x, const void* w, const float* bias, const void* residual, const moe_linear_dims* d,
+                  const moe_linear_cfg* cfg, void* y, uint32_t hold, moe_stream_t stream) {
     if (!d || !cfg) return refuse(MOE_ERR_NULL, "dims or cfg is NULL");
     if (d->M < 0 || d->N < 1 || d->K < 1) return refuse(MOE_ERR_SHAPE, "moe_linear: need M >= 0, N >= 1, K >= 1");
     constexpr int kMost = 1 << 24;
@@ -743,7 +742,7 @@ extern "C" moe_status moe_linear(const void* x, const void* w, const float* bias
     p.res_f32 = cfg->res_f32;
     p.y_f32 = cfg->y_f32;
     p.limit = cfg->swiglu_limit;
-    p.wait_limit = sm100::kWaitLimit;
+    p.hold = hold;
     p.err = device_info().err_word;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = cfg->act == MOE_ACT_NONE    ? run_linear<MOE_ACT_NONE>(c, p, s)
@@ -756,3 +755,25 @@ extern "C" moe_status moe_linear(const void* x, const void* w, const float* bias
     set_last_launch_count(1);
     return MOE_OK;
 }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_linear(const void* x, const void* w, const float* bias, const void* residual, const moe_linear_dims* d,
+                      const moe_linear_cfg* cfg, void* y, moe_stream_t stream) {
+    return linear(x, w, bias, residual, d, cfg, y, 0, stream);
+}
+
+moe_status moe_linear_expiry_check(const void* x, const void* w, const float* bias, const void* residual,
+                                   const moe_linear_dims* d, const moe_linear_cfg* cfg, void* y, uint32_t polls,
+                                   moe_stream_t stream) {
+    if (polls < 1 || polls > (1u << 20))
+        return refuse(MOE_ERR_SHAPE, "moe_linear_expiry_check: polls must be in [1, 2^20]");
+    return linear(x, w, bias, residual, d, cfg, y, polls, stream);
+}
+
+}  // extern "C"

@@ -78,3 +78,30 @@ def test_decode_layer_whose_grid_barriers_run_out(api, fmt, T, shared_I, given, 
         for a, b in zip(layer(D.x, logits=logits), want):
             assert torch.equal(a, b)
         assert api.moe_device_error() == 0
+
+
+@pytest.mark.parametrize("polls", [1, 4096])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("M,N,K", [(3, 200, 64), (8, 2048, 2048), (40, 5000, 1000), (130, 300, 300),   # one CTA or a cluster a tile
+                                   (700, 2048, 1024), (4096, 2048, 64), (2000, 1100, 5000)])           # SM pairs
+def test_linear_layer_whose_wait_runs_out(api, M, N, K, act, polls):
+    """The call records error 2 and ends, y keeps its bytes, and the next call is right."""
+    import ctypes
+
+    from sigmoid_top_routing_b200 import abi
+    rows, ld = (2 * N if act == "swiglu" else N), (K + 7) // 8 * 8
+    x = torch.randn(M, ld, device="cuda").bfloat16()[:, :K]
+    w = (torch.randn(rows, ld, device="cuda") * K ** -0.5).bfloat16()[:, :K]
+    want = api.moe_linear(x, w, act=act)
+    y = torch.full_like(want, 7.0)
+    d = abi.moe_linear_dims(M, N, K, ld, ld, 0, 0)
+    c = abi.moe_linear_cfg(abi.MOE_ACT_SWIGLU if act == "swiglu" else abi.MOE_ACT_NONE, 0, 0, 0.0)
+    for _ in range(2):
+        st = api.load().moe_linear_expiry_check(x.data_ptr(), w.data_ptr(), None, None, ctypes.byref(d), ctypes.byref(c),
+                                                y.data_ptr(), polls, torch.cuda.current_stream().cuda_stream)
+        assert st == abi.MOE_OK
+        torch.cuda.synchronize()
+        assert api.moe_device_error() == 2
+        assert (y == 7.0).all()
+        assert torch.equal(api.moe_linear(x, w, act=act), want)
+        assert api.moe_device_error() == 0

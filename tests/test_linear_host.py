@@ -67,3 +67,11 @@ def test_python_wrapper_needs_cuda():
     from sigmoid_top_routing_b200 import api
     with pytest.raises(ValueError):
         api.moe_linear(torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("polls", [0, (1 << 20) + 1])
+def test_expiry_check_refuses_its_polls(lib, polls):
+    d, c = abi.moe_linear_dims(4, 32, 64, 0, 0, 0, 0), abi.moe_linear_cfg(2, 0, 0, 0.0)
+    call = lib.moe_linear_expiry_check
+    assert call(0x10000, 0x20000, None, None, ctypes.byref(d), ctypes.byref(c), 0x30000, polls, None) == abi.MOE_ERR_SHAPE
+    assert call(0x10000, 0x20000, None, None, ctypes.byref(d), ctypes.byref(c), None, 1, None) == abi.MOE_ERR_NULL
