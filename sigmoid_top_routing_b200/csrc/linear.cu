@@ -37,12 +37,12 @@
 #include <cuda.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "internal.h"
 #include "launch.h"
 #include "sm100.cuh"
+#include "tmap.h"
 
 namespace moe {
 namespace {
@@ -558,36 +558,14 @@ __global__ void __launch_bounds__(kLinThreads)
 
 // ---------------------------------------------------------------------------- host side
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static EncodeFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* q = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r) ==
-                cudaSuccess &&
-            r == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeFn>(q);
-    });
-    return fn;
-}
-
 // bf16 rows in the 128-byte swizzle; halves > 1 adds a third dimension of that
 // many row blocks, `rows` rows apart.
 cudaError_t make_map(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t ld, uint32_t box_rows,
                      uint32_t halves) {
-    EncodeFn enc = encode_fn();
-    if (!enc) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {K, rows, halves}, strides[2] = {ld * 2, rows * ld * 2};
-    const cuuint32_t box[3] = {kBK, box_rows, halves}, ones[3] = {1, 1, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, halves > 1 ? 3 : 2, const_cast<void*>(base), dims,
-                           strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    const cuuint32_t box[3] = {kBK, box_rows, halves};
+    return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, halves > 1 ? 3 : 2, base, dims, strides, box,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 struct LinCall {
