@@ -281,3 +281,14 @@ def test_rows_beside_nan_and_infinite_rows(api, M, act):
     want, tol = formula(x[rows], w, b, r[rows], act, 0.0, torch.bfloat16)
     assert torch.isnan(y[1]).all()
     assert ((y[rows].double() - want).abs() <= tol).all()
+
+
+def test_more_than_2_to_the_31_elements(api):
+    """Offsets of y and of the residual past 32 bits, in place."""
+    M, N, K = 600_000, 4096, 64
+    x, w, b, _ = make(M, N, K, bias=True)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda").normal_()
+    rows = torch.tensor([0, 1, 262_143, 262_144, 524_287, 524_288, 599_999], device="cuda")   # 2^30 elements and multiples
+    want, tol = formula(x[rows], w, b, y[rows], "none", 0.0, torch.bfloat16)
+    api.moe_linear(x, w, b, y, y=y)
+    assert ((y[rows].double() - want).abs() <= tol).all()

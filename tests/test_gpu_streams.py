@@ -124,3 +124,48 @@ def test_workspace_outlives_its_layer_on_another_stream(api, block):
     blocks = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(4)]
     assert at not in [t.data_ptr() for t in blocks]
     same(got, want)
+
+
+def replayed(g, out, want):
+    for _ in range(3):
+        g.replay()
+    same(out, want)
+
+
+def test_first_calls_inside_a_capture(api, block):
+    """Token counts that the layer has not seen, a layer made there, and sizes of moe_linear never run before."""
+    wl, D = block
+    kw = dict(E=wl.E, k=wl.k, I=wl.I)
+    want = [t.clone() for t in api.DecodeLayer(D.W, D.w_router, D.expert_bias, **kw)(D.x)]
+    layer = api.DecodeLayer(D.W, D.w_router, D.expert_bias, **kw)
+    w = torch.randn(768, wl.H, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = [layer(D.x[:T]) for T in (3, 8)]
+        outs.append(api.DecodeLayer(D.W, D.w_router, D.expert_bias, **kw)(D.x[:5]))
+        lin = api.moe_linear(D.x, w, act="relu2")
+    for out in outs:
+        replayed(g, out, [t[:len(out[0])] for t in want])
+    same([lin], [api.moe_linear(D.x, w, act="relu2")])
+    assert api.moe_device_error() == 0
+
+
+def test_decode_layer_beside_other_streams_work(api, block):
+    """Its launch needs every SM at once; other streams keep them busy."""
+    wl, D = block
+    layer = api.DecodeLayer(D.W, D.w_router, D.expert_bias, E=wl.E, k=wl.k, I=wl.I)
+    x, w = torch.randn(8192, 1024, device="cuda").bfloat16(), torch.randn(2048, 1024, device="cuda").bfloat16()
+    want, lin = [t.clone() for t in layer(D.x)], api.moe_linear(x, w)
+    a, b, c = (torch.cuda.Stream() for _ in range(3))
+    torch.cuda.synchronize()
+    outs, lins = [], []
+    for _ in range(20):
+        outs.append(layer(D.x, stream=a))
+        lins.append(api.moe_linear(x, w, stream=b))
+        with torch.cuda.stream(c):
+            torch.mm(x, w.t())
+    for out in outs:
+        same(out, want)
+    same(lins, [lin] * len(lins))
+    assert api.moe_device_error() == 0
