@@ -354,7 +354,8 @@ def _check_weights(name: str, W: ExpertWeights, E: int, I: int, H: int, device) 
 
 
 class DecodeLayer:
-    """A whole MoE layer for a few tokens, one kernel launch a call (``moe_decode``).
+    """A whole MoE layer for a few tokens, one kernel launch a call (``moe_decode``;
+    from about 9 tokens with 4-bit experts, 12 with bf16 ones, ``moe_forward`` is faster).
 
     Holds what stays the same from step to step: the router, the experts, an
     optional shared expert (``Ws`` of width ``Is``, same format and activation),

@@ -35,12 +35,13 @@
 // Router sums carry ~46 bits (fp32 pairs) and close scores are compared in 64: E * H * T
 // is small here, and picks are then those of the real-number scores up to ties.
 //
-// Measured (device time of a call, weights rotated through more than L2; floor =
-// bytes at 6455 GB/s): 16 tokens, 32 experts, k = 4, 2048 x 1792, bf16: 93-97 us
-// (floor 96 by the expected number of active experts); 8 tokens 82 us (72); one token of relu^2 64 experts, k = 6, 2048 x 1024
-// with a shared expert 24 us (10.5); 4-bit 64 experts, k = 4, 2048 x 1536: one
-// affine token 21 us (3.4), five NVFP4 tokens 45 us (15); one token of a tiny
-// block 11 us.  Bound: HBM for bf16 from a few tokens on; the conversion of codes
+// Measured (calls in a row through DecodeLayer, weights rotated through more than
+// L2; the device's own time is ~1.5 us less; floor = bytes at 6455 GB/s): 16 tokens,
+// 32 experts, k = 4, 2048 x 1792, bf16: 91-101 us (floor 96 by the expected number of
+// active experts; moe_forward's tcgen05 tiles take 83); 8 tokens 72-84 us (72;
+// moe_forward 93); one token of relu^2 64 experts, k = 6, 2048 x 1024 with a shared
+// expert 26 us (10.5); 4-bit 64 experts, k = 4, 2048 x 1536: one affine token 22.6 us
+// (3.4), five NVFP4 tokens 45-48 us (15); one token of a tiny block 12.3 us.  Bound: HBM for bf16 from a few tokens on; the conversion of codes
 // (integer instructions at half rate) and the per-tile work for 4 bits; for one
 // token ~11 us of latency, a chain of a launch, two fenced grid barriers (~1.5 us
 // each), three dependent memory round trips and the selection.
@@ -725,8 +726,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const __grid_constant__ 
         }
         // ---- token rows into shared memory (while the other CTAs' logits arrive);
         // 4-bit experts: in f16, scaled by a power of two that brings the row's
-        // largest finite value to [2^14, 2^15) (smaller values than 2^-29 of that
-        // lose bits to f16's subnormals; infinities and NaN stay)
+        // largest finite value to [2^14, 2^15) (values below 2^-31 of that, in affine's
+        // odd pairs 2^-27, lose bits to f16's subnormals; infinities and NaN stay)
         float xscale = 1.0f;
         if (FMT != kBf16) {
             float m = 0.0f;

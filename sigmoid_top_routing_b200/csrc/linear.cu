@@ -23,12 +23,13 @@
 //                   distributed shared memory in rank order, so no workspace, no
 //                   atomics, and the same bits every time.
 //
-// Measured (device time): 8192 x 7168 (SwiGLU: 14336 rows) x 2048 320 us = 1502
-// TFLOP/s, 8192 x 2048 x 7168 with bias and residual 172 us = 1399 (a library
-// product of the same sizes, without epilogue, 346-430 and 159-217 us on the same
-// parts); 512 x 4096 x 2048 relu^2 10.6 us; 77 x 1537 x 1795 with fp32 residual
-// 7.8 us; 8 x 7168 (SwiGLU) x 2048 14.4 us = 4.1 TB/s; one token 2048 x 2048
-// 4.8-5.6 us.  Bound: the tensor cores at the large sizes (an SM takes ~75 GB/s of
+// Measured: 8192 x 7168 (SwiGLU: 14336 rows) x 2048 309 us = 1557 TFLOP/s in bursts,
+// 366-373 us = 1300 call after call at the power limit; 8192 x 2048 x 7168 with bias and
+// residual 162 us = 1484 and 192-195 us = 1250 (a library product of the same sizes,
+// without epilogue, 365-430 and 182-231 us); 512 x 4096 x 2048 relu^2 10.6 us; 77 x 1537
+// x 1795 with fp32 residual 7.8 us; 8 x 7168 (SwiGLU) x 2048 14.4 us = 4.1 TB/s; one token
+// 2048 x 2048 4.8-5.6 us.  (The last four are device times; calls in a row from Python
+// take 10.2-15 us, ~10 us of them on the host.)  Bound: the tensor cores at the large sizes (an SM takes ~75 GB/s of
 // operands per tile: 32 KB per 64 k at BN = 256), latency and the sharing of a
 // weight stream by uneven numbers of CTAs at the small ones.
 //

@@ -337,8 +337,8 @@ MOE_DEV void run_steps_f16(uint32_t w, uint32_t half, uint32_t x4, int s, int n,
     } else {
         const auto lo = [](uint32_t v) { return and_or(v, 0x000F000Fu, 0x64006400u); };
         const auto hi = [](uint32_t v) { return and_or(v, 0x00F000F0u, 0x64006400u); };
-// (unrolled twice the loop is slower: 1 token, 4 of 64 experts of 2048 x 1536,
-// 21.9 us to 20.9; NVFP4's is faster, 5 tokens 44.9 us to 45.3)
+        // (unrolled twice the loop is slower: 1 token, 4 of 64 experts of 2048 x 1536,
+        // 21.9 us to 20.9; NVFP4's is faster, 5 tokens 44.9 us to 45.3)
 #pragma unroll 1
         for (; n > 0; --n, ++s, sb += 2) {
             const uint32_t a = w + ((s & ~3) << 8) + (((s << 5) & 0x60) ^ x4);
