@@ -324,8 +324,8 @@ MOE_API moe_status moe_shared_expert_ex(const void* x, const moe_experts_w* Ws, 
  * to call).  It may serve any layer whose sizes need no more of it.  Calls that share it
  * must run on one device and not overlap on the GPU.  The launch is cooperative
  * (one CTA per SM, all resident); its waits are bounded: where one runs out the
- * call records device error 2 and ends without writing y, topk_idx and topk_w are
- * undefined, and the workspace serves the next call as it is. */
+ * call records device error 2 and ends with undefined outputs; the workspace serves
+ * the next call as it is. */
 #define MOE_DECODE_MAX_T 16
 typedef struct {
     const float* w_router;
@@ -353,7 +353,7 @@ MOE_API moe_status moe_decode_run(const moe_decode_plan* plan, const void* x, co
                                   size_t ws_bytes, moe_stream_t stream);
 /* moe_decode_run with the failure that its bounded waits are for, made without a
  * fault (as moe_wait_bound_check): the grid barriers wait for one arrival more than
- * comes and give up after `polls` polls, 1 to 2^20 (MOE_ERR_SHAPE). */
+ * comes and give up after `polls` polls, 1 to 2^20 (MOE_ERR_SHAPE).  y is not written. */
 MOE_API moe_status moe_decode_expiry_check(const moe_decode_plan* plan, const void* x, const float* logits,
                                            const void* residual, int32_t* topk_idx, float* topk_w, void* y,
                                            void* ws, size_t ws_bytes, uint32_t polls, moe_stream_t stream);

@@ -365,7 +365,7 @@ class DecodeLayer:
     replay at once, each need a layer of their own).  The tensors given here are
     kept, not copied: new values in them count from the next call on, other tensors
     set as fields of ``W`` or ``Ws`` do not.  Where a bounded wait of a call runs out
-    (``moe_device_error`` 2), its y is not written; the next call is not affected.
+    (``moe_device_error`` 2), its outputs are undefined; the next call is not affected.
     """
 
     def __init__(self, W: ExpertWeights, w_router=None, expert_bias=None, *, E: int, k: int, I: int,
