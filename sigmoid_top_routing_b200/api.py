@@ -395,7 +395,7 @@ class DecodeLayer:
         with torch.cuda.device(dev):
             if not torch.cuda.is_current_stream_capturing():
                 torch.cuda.current_stream().synchronize()         # the first call may be on any stream
-        self._seen = {torch._C._cuda_getCurrentRawStream(dev.index)}   # streams that the allocator knows of
+        self._seen = set()                                        # streams that the allocator knows of
         self._layer = abi.moe_layer(_ptr(w_router), _ptr(expert_bias), W.c_struct(),
                                     Ws.c_struct() if Ws is not None else abi.moe_experts_w(), Is, eps, router_scale,
                                     out_scale, router_cfg(score, norm_topk))

@@ -169,3 +169,26 @@ def test_decode_layer_beside_other_streams_work(api, block):
         same(out, want)
     same(lins, [lin] * len(lins))
     assert api.moe_device_error() == 0
+
+
+def test_weights_of_another_stream_outlive_their_layer(api, block):
+    """Weights allocated on one stream, a layer made and called on a second, then all of it dropped."""
+    wl, D = block
+    kw = dict(E=wl.E, k=wl.k, I=wl.I)
+    want = [t.clone() for t in api.DecodeLayer(D.W, D.w_router, D.expert_bias, **kw)(D.x)]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(a):
+        Wa = D.W.clone()
+    a.synchronize()
+    at = {Wa.w1.data_ptr(), Wa.w2.data_ptr()}
+    shapes = [Wa.w1.shape, Wa.w2.shape]
+    with torch.cuda.stream(b):
+        layer = api.DecodeLayer(Wa, D.w_router, D.expert_bias, **kw)
+        torch.cuda._sleep(CYCLES)
+        got = layer(D.x)
+    del Wa, layer
+    with torch.cuda.stream(a):
+        blocks = [torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in shapes for _ in range(4)]
+    assert not at & {t.data_ptr() for t in blocks}
+    same(got, want)
